@@ -327,6 +327,111 @@ kda_status kda_spec_commit(const kda_params* params, const void* k, const void* 
                            int32_t num_draft, const int32_t* accepted, float* state,
                            void* stream);
 
+/*
+ * kda_spec_accept -- verification of drafted tokens against the target's probabilities from
+ * given uniform random numbers; makes the `accepted` array that kda_spec_commit and
+ * kda_gdn_recurrent take.
+ *
+ * Sequence n has num_draft = K drafted tokens (0 <= K <= 64).  Draft j is kept while
+ *     uniforms[n][j] * q_j(x_j) < p_j(x_j)
+ * (q_j(x_j) = 1 where draft_probs is NULL: the drafts of a lookup are certain).  With a the
+ * number of drafts before the first that is not kept, one more token is drawn with
+ * uniforms[n][K]: from max(p_a - q_a, 0) where a draft was rejected (from p_a if that is zero
+ * everywhere), from p_a where all were kept.  The draw is the smallest i whose inclusive sum
+ * of weights exceeds uniforms[n][K] times their total.  Probabilities need not be normalised;
+ * entries that are negative or not a number weigh nothing.  Products and sums are fp64 and
+ * their order is fixed: the same inputs give the same tokens.
+ *
+ *   dtype        : kda_dtype of target_probs and draft_probs
+ *   target_probs : [num_seqs, K + 1, vocab], dense; row j is the distribution of the token
+ *                  that draft j proposes, row K that of the one behind the last draft
+ *   draft_probs  : [num_seqs, K, vocab], dense, or NULL
+ *   draft_tokens : int32 [num_seqs, K]; one outside [0, vocab) is rejected
+ *   uniforms     : fp32 [num_seqs, K + 1], each in [0, 1)
+ *   num_drafts   : int32 [num_seqs], DEVICE memory, drafts of each sequence (clamped to
+ *                  [0, K]; row num_drafts[n] of target_probs is then the last), or NULL: K
+ *   accepted     : int32 [num_seqs], out: kept drafts
+ *   tokens       : int32 [num_seqs, K + 1], out: the kept drafts, the drawn token, then -1
+ *                  (the drawn token is -1 if no entry has any weight)
+ *   workspace    : kda_spec_accept_workspace bytes, 16-byte aligned; contents on entry do
+ *                  not matter.  Calls that share one must be ordered on one stream.
+ * No output may overlap another argument.
+ */
+kda_status kda_spec_accept(int32_t dtype, int32_t num_seqs, int32_t num_draft, int64_t vocab,
+                           const void* target_probs, const void* draft_probs,
+                           const int32_t* draft_tokens, const float* uniforms,
+                           const int32_t* num_drafts, int32_t* accepted, int32_t* tokens,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace kda_spec_accept needs, or -1 if the arguments are invalid. */
+int64_t kda_spec_accept_workspace(int32_t num_seqs, int64_t vocab);
+
+/*
+ * The gated delta rule: the recurrence above with ONE log-decay per token and value head,
+ * and query and key heads shared by groups of value heads:
+ *     S  <- exp(log_alpha_t) S
+ *     S  <- S + beta_t k_t (v_t - S^T k_t)^T
+ *     o_t = S^T (scale q_t)
+ * Value head h reads query and key head h / (num_v_heads / num_k_heads).  log_alpha has no
+ * floor (any value <= 0, -inf included: the state is forgotten) and there is no output gate.
+ * q, k, v and out are params->dtype; log_alpha, beta and the states are fp32.
+ */
+typedef struct {
+    int32_t dtype;          /* kda_dtype of q, k, v and out                               */
+    int32_t num_k_heads;    /* query and key heads, >= 1                                  */
+    int32_t num_v_heads;    /* value heads, a multiple of num_k_heads                     */
+    int32_t dk;             /* key channels per head: 64 or 128                           */
+    int32_t dv;             /* value channels per head: 64 or 128                         */
+    float scale;            /* multiplies q (finite)                                      */
+    int64_t q_stride;       /* elements between tokens of q, k and v: 0 = dense, else at  */
+    int64_t k_stride;       /* least a token's heads and a multiple of 16 bytes (q, k and */
+    int64_t v_stride;       /* v as slices of one projection)                             */
+} kda_gdn_params;
+
+/*
+ * kda_gdn_chunk_prefill -- the gated delta rule over packed variable-length sequences.
+ *
+ *   q, k            : [T_total, num_k_heads, dk]   (token stride as params say)
+ *   v               : [T_total, num_v_heads, dv]
+ *   log_alpha, beta : fp32 [T_total, num_v_heads], dense
+ *   cu_seqlens_host : int32 [num_seqs + 1], host memory; starts at 0, does not decrease.  The
+ *                     call copies what it needs: no device copy is taken.
+ *   initial_state   : fp32 [num_seqs, num_v_heads, dk, dv] or NULL (zeros)
+ *   final_state     : as initial_state, or NULL (not written); may be the same pointer
+ *   out             : [T_total, num_v_heads, dv], dense
+ * A zero-length sequence writes no output rows and copies its initial state (or zeros).
+ * Nothing but out and final_state is written; neither may overlap an input (final_state may
+ * be initial_state).
+ */
+kda_status kda_gdn_chunk_prefill(const kda_gdn_params* params, const void* q, const void* k,
+                                 const void* v, const float* log_alpha, const float* beta,
+                                 const int32_t* cu_seqlens_host, int32_t num_seqs,
+                                 const float* initial_state, float* final_state, void* out,
+                                 void* stream);
+
+/*
+ * kda_gdn_recurrent -- num_tokens = K tokens (1 <= K <= 16) of every sequence from its stored
+ * state, token by token: decoding (K = 1), the outputs of drafts (update_state = 0) and the
+ * commit of their kept prefix (steps, out = NULL).
+ *
+ *   q, k            : [num_seqs * K, num_k_heads, dk];  v, out : [num_seqs * K, num_v_heads, dv]
+ *   log_alpha, beta : fp32 [num_seqs * K, num_v_heads]    (row n*K + j is token j of sequence n)
+ *   steps           : int32 [num_seqs], DEVICE memory: the stored state advances over the first
+ *                     steps[n] tokens (clamped to [0, K]; 0 leaves it untouched), or NULL: all
+ *   state_indices   : int32 [num_seqs], DEVICE memory: sequence n's state is state[index], or
+ *                     NULL: state[n].  An index outside [0, num_slots) marks a padded row: no
+ *                     state is touched and its outputs are zero.  Where the states are written,
+ *                     a row that names a slot an earlier row has named is a padded row too.
+ *   state           : fp32 [num_slots, num_v_heads, dk, dv], read and written in place (only
+ *                     read if update_state is 0)
+ *   out             : may be NULL (no outputs); overlaps no other argument
+ */
+kda_status kda_gdn_recurrent(const kda_gdn_params* params, const void* q, const void* k,
+                             const void* v, const float* log_alpha, const float* beta,
+                             int32_t num_seqs, int32_t num_tokens, const int32_t* steps,
+                             const int32_t* state_indices, int32_t num_slots, float* state,
+                             int32_t update_state, void* out, void* stream);
+
 /* Static English text for a status code (never NULL). */
 const char* kda_status_string(kda_status status);
 

@@ -13,7 +13,8 @@ EXPORTED = ("kda_chunk_prefill", "kda_chunk_prefill_checkpointed", "kda_decode_s
             "kda_spec_verify", "kda_spec_commit", "kda_chunk_prefill_segmented",
             "kda_prefill_segmented_workspace", "kda_chunk_prefill_segmented_noalloc",
             "kda_noalloc_scratch_bytes", "kda_prefill_segment_plan", "kda_prefill_backward",
-            "kda_prefill_backward_workspace", "kda_status_string", "kda_last_error",
+            "kda_prefill_backward_workspace", "kda_spec_accept", "kda_spec_accept_workspace",
+            "kda_gdn_chunk_prefill", "kda_gdn_recurrent", "kda_status_string", "kda_last_error",
             "kda_abi_version")
 
 
@@ -21,6 +22,13 @@ class KdaParams(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("num_heads", ctypes.c_int32),
                 ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("chunk", ctypes.c_int32),
                 ("log_alpha_floor", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class GdnParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("num_k_heads", ctypes.c_int32),
+                ("num_v_heads", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
 
 
 class KdaError(RuntimeError):
@@ -78,6 +86,15 @@ def load() -> ctypes.CDLL:
     lib.kda_prefill_backward_workspace.argtypes = [ctypes.POINTER(KdaParams),
                                                    ctypes.POINTER(I32), I32]
     lib.kda_prefill_backward_workspace.restype = ctypes.c_int64
+    I64, G = ctypes.c_int64, ctypes.POINTER(GdnParams)
+    lib.kda_spec_accept.argtypes = [I32, I32, I32, I64, P, P, P, P, P, P, P, P, I64, P]
+    lib.kda_spec_accept.restype = ctypes.c_int
+    lib.kda_spec_accept_workspace.argtypes = [I32, I64]
+    lib.kda_spec_accept_workspace.restype = I64
+    lib.kda_gdn_chunk_prefill.argtypes = [G, P, P, P, P, P, ctypes.POINTER(I32), I32, P, P, P, P]
+    lib.kda_gdn_chunk_prefill.restype = ctypes.c_int
+    lib.kda_gdn_recurrent.argtypes = [G, P, P, P, P, P, I32, I32, P, P, I32, P, I32, P, P]
+    lib.kda_gdn_recurrent.restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_last_error.argtypes = []

@@ -1,0 +1,286 @@
+// gdn_recurrent.hip -- the gated delta rule token by token, state in registers (gfx950).
+//
+// Per (sequence, value head), one log-decay g_t per token:
+//   S <- e^{g_t} S;  u = beta_t (v_t - S^T k_t);  S <- S + k_t u^T;  o_t = scale S^T q_t
+// With w = S^T k and b = S^T (scale q) of the state BEFORE the decay, a = e^{g}:
+//   u = beta (v - a w),   o = a b + (k . scale q) u,   S <- a S + k u^T
+// so one pass over the state serves the erase, the write and the readout, and both column
+// sums share one reduction.
+//
+// Two uses.  The step (1..16 tokens per sequence, the serving form): the state is the large
+// operand, read once and written once whatever the number of tokens; HBM-bound.  The
+// sequential prefill (any length, the form of 32-bit inputs): the state stays in registers
+// for the whole sequence and the tokens stream through LDS in blocks of 16, one barrier per
+// token; bound by that barrier and the two reductions (see the table in launch below).
+//
+// A workgroup of four waves owns NV value columns of one state.  Thread t holds columns
+// 4 (t % COLG) .. +3 of RPT consecutive rows, so a row of the slice is read and written by
+// COLG consecutive threads as one contiguous segment and a thread's k and q come from LDS
+// as 16-byte reads.  Everything is fp32; outputs are rounded once to their type.
+#include "gdn_launch.h"
+#include "kda_device.h"
+#include "kda_launch.h"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int TB = 16;  // tokens staged at a time
+
+struct RecArgs {
+    const void *q, *k, *v;
+    const float *la, *be;
+    int64_t qs, ks, vs;
+    int hk, hv;
+    float scale;
+    void* out;
+    // step form
+    int num_tokens, num_slots, num_seqs;
+    const int32_t *steps, *slots;
+    float* state;
+    bool update;
+    // sequential prefill
+    const float* S0;
+    float* Sf;
+};
+
+__device__ inline f32x4 load4f(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ inline f32x4 load4f(const bf16* p) {
+    return __builtin_convertvector(*reinterpret_cast<const bf16x4*>(p), f32x4);
+}
+
+template <typename T, int DK, int DV, int NV>
+struct Tile {
+    static constexpr int COLG = NV / 4, ROWG = kThreads / COLG, RPT = DK / ROWG;
+    static constexpr int QV = TB * DK / 4 / kThreads;  // 16-byte pieces of q (and k) per thread
+    static constexpr int VV = TB * NV / 4 / kThreads > 0 ? TB * NV / 4 / kThreads : 1;
+    static_assert(DK % ROWG == 0 && RPT % 2 == 0, "shape");
+};
+
+// The tokens' rows on their way from memory to LDS: loaded before a block of tokens is
+// worked on, stored after it.
+template <typename T, int DK, int DV, int NV>
+struct Stage {
+    using L = Tile<T, DK, DV, NV>;
+    f32x4 q[L::QV], k[L::QV], v[L::VV];
+    float g, b;
+    __device__ void load(const RecArgs& A, int64_t row0, int n, int hk, int hv, int col0) {
+        const int t = threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < L::QV; ++i) {
+            const int e = t + kThreads * i, r = e / (DK / 4), c = 4 * (e % (DK / 4));
+            q[i] = k[i] = zero4();
+            if (r < n) {
+                q[i] = load4f((const T*)A.q + (row0 + r) * A.qs + (int64_t)hk * DK + c);
+                k[i] = load4f((const T*)A.k + (row0 + r) * A.ks + (int64_t)hk * DK + c);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < L::VV; ++i) {
+            const int e = t + kThreads * i, r = e / (NV / 4), c = 4 * (e % (NV / 4));
+            v[i] = zero4();
+            if (r < n) v[i] = load4f((const T*)A.v + (row0 + r) * A.vs + (int64_t)hv * DV + col0 + c);
+        }
+        g = b = 0.f;
+        if (t < n) {
+            g = A.la[(row0 + t) * A.hv + hv];
+            b = A.be[(row0 + t) * A.hv + hv];
+        }
+    }
+};
+
+// one sequence's tokens from row0 on; `advance` tokens move the stored state (to Sout),
+// outputs are written where `out` is given
+template <typename T, int DK, int DV, int NV>
+__device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t row0, int n,
+                     int advance, T* out, int head, int col0, bool skip_check, int slot_seq) {
+    using L = Tile<T, DK, DV, NV>;
+    __shared__ __attribute__((aligned(16))) float s_k[TB][DK], s_q[TB][DK], s_v[TB][NV];
+    __shared__ float s_a[TB], s_b[TB], s_kq[TB];
+    __shared__ f32x4 s_red[2][4][L::COLG][2];
+    const int t = threadIdx.x, cg = t % L::COLG, rg = t / L::COLG, wave = t / 64, lane = t % 64;
+    const int hk = head / (A.hv / A.hk);
+
+    // the state's loads first: the long-latency part of a step
+    f32x4 s[L::RPT];
+    const int64_t at = (int64_t)(rg * L::RPT) * DV + col0 + 4 * cg;
+#pragma unroll
+    for (int i = 0; i < L::RPT; ++i)
+        s[i] = Sin ? *reinterpret_cast<const f32x4*>(Sin + at + i * DV) : zero4();
+    Stage<T, DK, DV, NV> st;
+    st.load(A, row0, min(n, TB), hk, head, col0);
+    bool twice = false;  // an earlier row of this call names the same slot
+    if (skip_check) {
+        for (int j = t; j < slot_seq; j += kThreads) twice |= A.slots[j] == A.slots[slot_seq];
+        if (__syncthreads_or(twice)) {
+            if (out)
+                for (int j = t; j < n * (NV / 4); j += kThreads)
+                    store4(out + (row0 + j / (NV / 4)) * (int64_t)A.hv * DV + (int64_t)head * DV +
+                               col0 + 4 * (j % (NV / 4)), Mma<T>::pack(zero4()));
+            return;
+        }
+    }
+    auto put = [&]() {
+        if (!Sout) return;
+        // non-temporal: the state is not read again by this call
+#pragma unroll
+        for (int i = 0; i < L::RPT; ++i)
+            __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(Sout + at + i * DV));
+    };
+    if (advance == 0 && Sout != Sin) put();
+    for (int t0 = 0; t0 < n; t0 += TB) {
+        const int m = min(n - t0, TB);
+        __syncthreads();  // the block before is done with the tiles
+#pragma unroll
+        for (int i = 0; i < L::QV; ++i) {
+            const int e = t + kThreads * i, r = e / (DK / 4), c = 4 * (e % (DK / 4));
+            *reinterpret_cast<f32x4*>(&s_k[r][c]) = st.k[i];
+            *reinterpret_cast<f32x4*>(&s_q[r][c]) = st.q[i] * A.scale;
+        }
+#pragma unroll
+        for (int i = 0; i < L::VV; ++i) {
+            const int e = t + kThreads * i, r = e / (NV / 4), c = 4 * (e % (NV / 4));
+            if (r < TB) *reinterpret_cast<f32x4*>(&s_v[r][c]) = st.v[i];
+        }
+        if (t < TB) {
+            s_a[t] = expf(st.g);
+            s_b[t] = st.b;
+        }
+        __syncthreads();
+        if (t0 + TB < n) st.load(A, row0 + t0 + TB, min(n - t0 - TB, TB), hk, head, col0);
+        if (out) {  // k . (scale q) of every token: 16 lanes each
+            float kq = 0.f;
+#pragma unroll
+            for (int c = 0; c < DK / 16; ++c)
+                kq += s_k[t / 16][t % 16 + 16 * c] * s_q[t / 16][t % 16 + 16 * c];
+#pragma unroll
+            for (int off = 8; off >= 1; off >>= 1) kq += __shfl_xor(kq, off);
+            if (t % 16 == 0) s_kq[t / 16] = kq;  // read behind the next barrier
+        }
+        for (int j = 0; j < m; ++j) {
+            f32x4 w = zero4(), b = zero4();
+#pragma unroll
+            for (int i = 0; i < L::RPT; ++i) {
+                w += s[i] * s_k[j][rg * L::RPT + i];
+                b += s[i] * s_q[j][rg * L::RPT + i];
+            }
+#pragma unroll
+            for (int off = L::COLG; off < 64; off <<= 1) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    w[c] += __shfl_xor(w[c], off);
+                    b[c] += __shfl_xor(b[c], off);
+                }
+            }
+            if (lane < L::COLG) {
+                s_red[j & 1][wave][lane][0] = w;
+                s_red[j & 1][wave][lane][1] = b;
+            }
+            __syncthreads();
+            w = (s_red[j & 1][0][cg][0] + s_red[j & 1][1][cg][0]) +
+                (s_red[j & 1][2][cg][0] + s_red[j & 1][3][cg][0]);
+            b = (s_red[j & 1][0][cg][1] + s_red[j & 1][1][cg][1]) +
+                (s_red[j & 1][2][cg][1] + s_red[j & 1][3][cg][1]);
+            const float a = s_a[j];
+            const f32x4 u = s_b[j] * (*reinterpret_cast<const f32x4*>(&s_v[j][4 * cg]) - a * w);
+#pragma unroll
+            for (int i = 0; i < L::RPT; ++i) s[i] = a * s[i] + s_k[j][rg * L::RPT + i] * u;
+            if (out && rg == 0)
+                store4(out + (row0 + t0 + j) * (int64_t)A.hv * DV + (int64_t)head * DV + col0 + 4 * cg,
+                       Mma<T>::pack(a * b + s_kq[j] * u));
+            if (t0 + j + 1 == advance) {
+                put();
+                if (!out) return;  // (the whole workgroup: advance is the same for all)
+            }
+        }
+    }
+}
+
+template <typename T, int DK, int DV, int NV>
+__global__ __launch_bounds__(kThreads) void step_kernel(const RecArgs A) {
+    constexpr int SL = DV / NV;
+    const int64_t pair = blockIdx.x / SL;
+    const int n = (int)(pair / A.hv), head = (int)(pair % A.hv), col0 = NV * (int)(blockIdx.x % SL);
+    const int64_t row0 = (int64_t)n * A.num_tokens;
+    T* out = (T*)A.out;
+    const int slot = A.slots ? A.slots[n] : n;
+    if (slot < 0 || slot >= A.num_slots) {  // a padded row: no state, zero outputs
+        if (out)
+            for (int j = threadIdx.x; j < A.num_tokens * (NV / 4); j += kThreads)
+                store4(out + (row0 + j / (NV / 4)) * (int64_t)A.hv * DV + (int64_t)head * DV + col0 +
+                           4 * (j % (NV / 4)), Mma<T>::pack(zero4()));
+        return;
+    }
+    int adv = A.update ? A.num_tokens : 0;
+    if (A.update && A.steps) adv = min(max(A.steps[n], 0), A.num_tokens);
+    if (adv == 0 && !out) return;
+    float* S = A.state + ((int64_t)slot * A.hv + head) * (int64_t)(DK * DV);
+    walk<T, DK, DV, NV>(A, S, S, row0, A.num_tokens, adv, out, head, col0, A.update && A.slots, n);
+}
+
+template <typename T, int DK, int DV, int NV>
+__global__ __launch_bounds__(kThreads) void seq_kernel(const RecArgs A, const GdnTable tab) {
+    constexpr int SL = DV / NV;
+    const int64_t pair = blockIdx.x / SL;
+    const int i = (int)(pair / A.hv), head = (int)(pair % A.hv), col0 = NV * (int)(blockIdx.x % SL);
+    const int64_t ss = ((int64_t)tab.id[i] * A.hv + head) * (int64_t)(DK * DV);
+    walk<T, DK, DV, NV>(A, A.S0 ? A.S0 + ss : nullptr, A.Sf ? A.Sf + ss : nullptr, tab.start[i],
+                        tab.len[i], tab.len[i], (T*)A.out, head, col0, false, 0);
+}
+
+// f(T, DK, DV, NV) for the call's type and shapes
+template <typename F>
+hipError_t dispatch(const GdnDims& d, int nv, F&& f) {
+    auto nvs = [&](auto t, auto dk, auto dv) {
+        if (nv == 32) return f(t, dk, dv, std::integral_constant<int, 32>{});
+        return f(t, dk, dv, dv);
+    };
+    auto dvs = [&](auto t, auto dk) {
+        if (d.dv == 128) return nvs(t, dk, std::integral_constant<int, 128>{});
+        return nvs(t, dk, std::integral_constant<int, 64>{});
+    };
+    auto dks = [&](auto t) {
+        if (d.dk == 128) return dvs(t, std::integral_constant<int, 128>{});
+        return dvs(t, std::integral_constant<int, 64>{});
+    };
+    return d.dtype == DTYPE_BF16 ? dks(bf16{}) : dks(float{});
+}
+
+RecArgs common(const GdnDims& d) {
+    RecArgs r = {};
+    r.qs = d.qs; r.ks = d.ks; r.vs = d.vs; r.hk = d.hk; r.hv = d.hv; r.scale = d.scale;
+    return r;
+}
+
+}  // namespace
+
+hipError_t launch_gdn_recurrent(const GdnRecurrentArgs& a, hipStream_t stream) {
+    RecArgs r = common(a.d);
+    r.q = a.q; r.k = a.k; r.v = a.v; r.la = a.log_alpha; r.be = a.beta; r.out = a.out;
+    r.num_tokens = a.num_tokens; r.num_slots = a.num_slots; r.num_seqs = a.num_seqs;
+    r.steps = a.steps; r.slots = a.state_indices; r.state = a.state; r.update = a.update;
+    const int64_t blocks = (int64_t)a.num_seqs * a.d.hv * (a.d.dv / a.nv);
+    if (blocks == 0) return hipSuccess;
+    return dispatch(a.d, a.nv, [&](auto t, auto dk, auto dv, auto nv) {
+        hipLaunchKernelGGL((step_kernel<decltype(t), decltype(dk)::value, decltype(dv)::value,
+                                        decltype(nv)::value>),
+                           dim3((unsigned)blocks), dim3(kThreads), 0, stream, r);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_gdn_sequential(const GdnPrefillArgs& a, const GdnTable& tab, hipStream_t stream) {
+    RecArgs r = common(a.d);
+    r.q = a.q; r.k = a.k; r.v = a.v; r.la = a.log_alpha; r.be = a.beta; r.out = a.out;
+    r.S0 = a.initial_state; r.Sf = a.final_state;
+    const int64_t blocks = (int64_t)a.num_seqs * a.d.hv * (a.d.dv / a.nv);
+    if (blocks == 0) return hipSuccess;
+    return dispatch(a.d, a.nv, [&](auto t, auto dk, auto dv, auto nv) {
+        hipLaunchKernelGGL((seq_kernel<decltype(t), decltype(dk)::value, decltype(dv)::value,
+                                       decltype(nv)::value>),
+                           dim3((unsigned)blocks), dim3(kThreads), 0, stream, r, tab);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace kda

@@ -6,48 +6,24 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstdlib>
 #include <numeric>
 #include <string>
 #include <vector>
 
 #include "../../include/kda.h"
+#include "kda_check.h"
 #include "kda_launch.h"
 
+using kda::check_ptr;
+using kda::device_cu_count;
+using kda::fail;
+using kda::ok;
+using kda::overlaps;
+using kda::Range;
+using kda::range;
+
 namespace {
-
-thread_local std::string g_last_error;
-
-kda_status fail(kda_status s, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return s;
-}
-
-kda_status ok() {
-    g_last_error.clear();
-    return KDA_OK;
-}
-
-struct Range {
-    const char* name;
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-bool overlaps(const Range& a, const Range& b) {
-    return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
-}
-
-Range range(const char* name, const void* p, uint64_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{name, lo, p ? lo + bytes : lo};
-}
 
 kda_status check_params(const kda_params* p) {
     if (!p) return fail(KDA_ERR_INVALID_ARGUMENT, "params is NULL");
@@ -66,26 +42,6 @@ kda_status check_params(const kda_params* p) {
     return KDA_OK;
 }
 
-kda_status check_ptr(const char* name, const void* ptr, size_t align) {
-    if (!ptr) return fail(KDA_ERR_INVALID_ARGUMENT, "%s is NULL", name);
-    if (reinterpret_cast<uintptr_t>(ptr) % align)
-        return fail(KDA_ERR_INVALID_ARGUMENT, "%s is not %zu-byte aligned", name, align);
-    return KDA_OK;
-}
-
-int device_cu_count() {
-    static int cached = 0;
-    if (cached) return cached;
-    int dev = 0, cus = 0;
-    if (hipGetDevice(&dev) == hipSuccess &&
-        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess &&
-        cus > 0)
-        cached = cus;
-    else
-        cached = 256;
-    return cached;
-}
-
 }  // namespace
 
 extern "C" {
@@ -100,7 +56,7 @@ const char* kda_status_string(kda_status s) {
     return "unknown status";
 }
 
-const char* kda_last_error(void) { return g_last_error.c_str(); }
+const char* kda_last_error(void) { return kda::last_error().c_str(); }
 
 int32_t kda_abi_version(void) { return KDA_ABI_VERSION; }
 

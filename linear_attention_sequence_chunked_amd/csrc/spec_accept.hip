@@ -1,0 +1,234 @@
+// spec_accept.hip -- verification of drafted tokens against the target's probabilities
+// from given uniform random numbers (gfx950).
+//
+// Sequence n has K drafts x_j with draft probabilities q_j (or none: a draft is then a
+// certain one, q_j(x_j) = 1) and target probabilities p_0 .. p_K.  Draft j is kept while
+//   u_j q_j(x_j) < p_j(x_j);
+// a = the number kept before the first that is not.  The next token is drawn with u_K from
+//   r = max(p_a - q_a, 0)  if a draft was rejected at a (p_a if r is zero everywhere),
+//   r = p_a                if all were kept,
+// as the smallest i with r_0 + .. + r_i > u_K sum(r).  All products, differences and sums
+// are fp64: the products and differences of fp32 values are exact there, and a draw is
+// decided by where a sum over the whole vocabulary crosses a border.
+//
+// Bound by reading one row of p and one of q per sequence; everything else is latency.  The
+// vocabulary is cut into pieces, so that one sequence also spreads over the card: a first
+// launch sums each piece, a second finds the piece that holds the draw from the sums (in
+// piece order: the same result whatever ran first) and scans that piece alone.
+#include "gdn_launch.h"
+#include "kda_device.h"
+#include "kda_launch.h"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+
+// kept drafts of sequence n (every lane of wave 0 returns it); x: the rejected draft, or -1
+template <typename T>
+__device__ int count_kept(const AcceptArgs& A, int n, int lane, bool* rejected) {
+    int m = A.num_draft;
+    if (A.num_drafts) m = min(max(A.num_drafts[n], 0), A.num_draft);
+    bool keep = false;
+    if (lane < m) {
+        const int64_t row = (int64_t)n * (A.num_draft + 1) + lane, drow = (int64_t)n * A.num_draft + lane;
+        const int64_t x = A.tokens[drow];
+        if (x >= 0 && x < A.vocab) {  // a token outside the vocabulary is rejected, never read
+            const double px = to_f32(((const T*)A.p)[row * A.vocab + x]);
+            const double qx = A.q ? (double)to_f32(((const T*)A.q)[drow * A.vocab + x]) : 1.0;
+            keep = (double)A.uniforms[row] * qx < px;
+        }
+    }
+    const unsigned long long miss = ~__ballot(keep);  // lanes >= m miss
+    const int a = miss ? (int)__builtin_ctzll(miss) : 64;
+    *rejected = a < m;
+    return a;
+}
+
+// the entry's weight in the draw, and in the fallback (p alone)
+struct Weights {
+    double r, p;
+};
+template <typename T>
+__device__ inline Weights weights(const T* p, const T* q, int64_t i, int64_t certain) {
+    const double pv = to_f32(p[i]);
+    Weights w;
+    w.p = pv > 0.0 ? pv : 0.0;
+    w.r = w.p;
+    if (q) {
+        const double d = pv - (double)to_f32(q[i]);
+        w.r = d > 0.0 ? d : 0.0;  // NaN counts as nothing
+    }
+    if (i == certain) w.r = 0.0;
+    return w;
+}
+
+__device__ inline double wave_sum(double x) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off);
+    return x;
+}
+
+struct Row {
+    int kept;
+    bool rejected;
+};
+
+template <typename T>
+__device__ Row find_row(const AcceptArgs& A, int n) {
+    __shared__ int s_row[2];
+    if (threadIdx.x < 64) {
+        bool rej;
+        const int a = count_kept<T>(A, n, threadIdx.x, &rej);
+        if (threadIdx.x == 0) {
+            s_row[0] = a;
+            s_row[1] = rej;
+        }
+    }
+    __syncthreads();
+    return Row{s_row[0], s_row[1] != 0};
+}
+
+template <typename T>
+__device__ void row_of(const AcceptArgs& A, int n, const Row& R, const T*& p, const T*& q, int64_t& certain) {
+    p = (const T*)A.p + ((int64_t)n * (A.num_draft + 1) + R.kept) * A.vocab;
+    q = nullptr;
+    certain = -1;
+    if (R.rejected) {
+        const int64_t drow = (int64_t)n * A.num_draft + R.kept;
+        if (A.q) q = (const T*)A.q + drow * A.vocab;
+        else certain = A.tokens[drow];
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void sum_kernel(const AcceptArgs A) {
+    __shared__ double s_sum[4][2];
+    const int n = blockIdx.x / A.pieces, piece = blockIdx.x % A.pieces;
+    const Row R = find_row<T>(A, n);
+    const T *p, *q;
+    int64_t certain;
+    row_of(A, n, R, p, q, certain);
+    const int64_t lo = piece * A.piece, hi = min(lo + A.piece, A.vocab);
+    double sr = 0.0, sp = 0.0;
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+        const Weights w = weights(p, q, i, certain);
+        sr += w.r;
+        sp += w.p;
+    }
+    sr = wave_sum(sr);
+    sp = wave_sum(sp);
+    if (threadIdx.x % 64 == 0) {
+        s_sum[threadIdx.x / 64][0] = sr;
+        s_sum[threadIdx.x / 64][1] = sp;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2)
+        A.partial[2 * (int64_t)blockIdx.x + threadIdx.x] =
+            (s_sum[0][threadIdx.x] + s_sum[1][threadIdx.x]) + (s_sum[2][threadIdx.x] + s_sum[3][threadIdx.x]);
+}
+
+// inclusive scan over the workgroup's 256 values; total in `all`
+__device__ double scan(double x, double* s_wave, double& all) {
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double y = __shfl_up(x, off);
+        if (lane >= off) x += y;
+    }
+    __syncthreads();
+    if (lane == 63) s_wave[wave] = x;
+    __syncthreads();
+    double before = 0.0;
+    for (int w = 0; w < wave; ++w) before += s_wave[w];
+    all = ((s_wave[0] + s_wave[1]) + s_wave[2]) + s_wave[3];
+    return before + x;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void draw_kernel(const AcceptArgs A) {
+    __shared__ double s_wave[4];
+    __shared__ double s_before;
+    __shared__ int s_piece, s_pos, s_last;
+    __shared__ long long s_at, s_end;
+    const int n = blockIdx.x, t = threadIdx.x;
+    const Row R = find_row<T>(A, n);
+    const T *p, *q;
+    int64_t certain;
+    row_of(A, n, R, p, q, certain);
+    if (t == 0) {
+        s_piece = A.pieces;
+        s_last = -1;
+        s_at = A.vocab;
+        s_end = -1;
+    }
+    // the piece that holds the draw: the first whose inclusive sum exceeds u * total
+    double mine = t < A.pieces ? A.partial[2 * ((int64_t)n * A.pieces + t)] : 0.0, all;
+    double inc = scan(mine, s_wave, all);
+    const bool plain = !(all > 0.0);  // nothing left: draw from p
+    if (plain) {
+        mine = t < A.pieces ? A.partial[2 * ((int64_t)n * A.pieces + t) + 1] : 0.0;
+        inc = scan(mine, s_wave, all);
+    }
+    const double u = (double)A.uniforms[(int64_t)n * (A.num_draft + 1) + A.num_draft];
+    const double target = u * all;
+    if (mine > 0.0) {
+        if (inc > target) atomicMin(&s_piece, t);
+        atomicMax(&s_last, t);
+    }
+    __syncthreads();
+    const int piece = s_piece < A.pieces ? s_piece : s_last;  // u * total not below any sum: the last entry
+    if (t == piece) s_before = s_piece < A.pieces ? inc - mine : 0.0;
+    __syncthreads();
+    int64_t drawn = -1;
+    if (piece >= 0) {  // -1: no entry has any weight
+        const int64_t lo = piece * A.piece, hi = min(lo + A.piece, A.vocab);
+        const int64_t per = (hi - lo + kThreads - 1) / kThreads;
+        const int64_t a = min(lo + t * per, hi), b = min(a + per, hi);
+        double sum = 0.0;
+        for (int64_t i = a; i < b; ++i) {
+            const Weights w = weights(p, q, i, certain);
+            sum += plain ? w.p : w.r;
+        }
+        double local_all;
+        double end = s_before + scan(sum, s_wave, local_all);
+        double c = end - sum;
+        int64_t first = A.vocab, last = -1;
+        for (int64_t i = a; i < b; ++i) {
+            const Weights w = weights(p, q, i, certain);
+            const double x = plain ? w.p : w.r;
+            c += x;
+            if (x > 0.0) {
+                if (c > target && first == A.vocab) first = i;
+                last = i;
+            }
+        }
+        if (first < A.vocab) atomicMin(&s_at, (long long)first);
+        if (last >= 0) atomicMax(&s_end, (long long)last);
+        __syncthreads();
+        drawn = (s_piece < A.pieces && s_at < A.vocab) ? s_at : s_end;
+    }
+    if (t == 0) A.accepted[n] = R.kept;
+    for (int j = t; j <= A.num_draft; j += kThreads)
+        A.out[(int64_t)n * (A.num_draft + 1) + j] =
+            j < R.kept ? A.tokens[(int64_t)n * A.num_draft + j] : (j == R.kept ? (int32_t)drawn : -1);
+}
+
+template <typename T>
+hipError_t launch_typed(const AcceptArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL((sum_kernel<T>), dim3((unsigned)(a.num_seqs * (int64_t)a.pieces)), dim3(kThreads), 0,
+                       stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((draw_kernel<T>), dim3((unsigned)a.num_seqs), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_accept(const AcceptArgs& a, hipStream_t stream) {
+    if (a.num_seqs == 0) return hipSuccess;
+    return a.dtype == DTYPE_BF16 ? launch_typed<bf16>(a, stream) : launch_typed<float>(a, stream);
+}
+
+}  // namespace kda
