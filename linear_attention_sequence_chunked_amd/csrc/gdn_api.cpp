@@ -52,8 +52,8 @@ kda_status check_gdn(const kda_gdn_params* p, kda::GdnDims& d) {
         if (s[i] < dense[i] || s[i] % vec)
             return fail(KDA_ERR_INVALID_ARGUMENT, "%s %lld: at least %lld and a multiple of %lld is needed",
                         names[i], (long long)given[i], (long long)dense[i], (long long)vec);
-        if (s[i] > INT32_MAX)
-            return fail(KDA_ERR_UNSUPPORTED, "%s %lld exceeds 2^31 - 1", names[i], (long long)given[i]);
+        if (s[i] > 1 << 23)  // a chunk's 64 rows stay within 32-bit offsets
+            return fail(KDA_ERR_UNSUPPORTED, "%s %lld exceeds 2^23", names[i], (long long)given[i]);
     }
     d = kda::GdnDims{p->dtype, p->num_k_heads, p->num_v_heads, p->dk, p->dv, p->scale, s[0], s[1], s[2]};
     return KDA_OK;
@@ -162,12 +162,14 @@ kda_status kda_gdn_chunk_prefill(const kda_gdn_params* params, const void* q, co
         if ((st = check_grid(std::min<int64_t>(num_seqs, kda::kGdnSeqs) * d.hv * (d.dv / 16))) != KDA_OK) return st;
         a.q = q; a.k = k; a.v = v; a.log_alpha = log_alpha; a.beta = beta;
         a.initial_state = initial_state; a.final_state = final_state; a.out = out;
-        a.nv = kda::gdn_recurrent_nv(d.dv, pairs, cus);
+        const bool chunked = d.dtype == KDA_DTYPE_BF16;
+        a.nv = chunked ? kda::gdn_prefill_nv(d.dv, pairs, cus) : kda::gdn_recurrent_nv(d.dv, pairs, cus);
         const std::vector<int32_t> order = longest_first(cu_seqlens_host, num_seqs);
         kda::GdnTable tab;
         for (int32_t from = 0; from < num_seqs; from += a.num_seqs) {
             a.num_seqs = fill_table(tab, cu_seqlens_host, order, from);
-            const hipError_t e = kda::launch_gdn_sequential(a, tab, reinterpret_cast<hipStream_t>(stream));
+            const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+            const hipError_t e = chunked ? kda::launch_gdn_chunked(a, tab, hs) : kda::launch_gdn_sequential(a, tab, hs);
             if (e != hipSuccess)
                 return fail(KDA_ERR_HIP, "kda_gdn_chunk_prefill launch: %s", hipGetErrorString(e));
         }

@@ -65,11 +65,14 @@ struct AcceptArgs {
 
 // value columns per workgroup of the token-by-token kernel (gdn_plan.cpp)
 int gdn_recurrent_nv(int dv, int64_t pairs, int cu_count);
+// value columns per workgroup of the chunked prefill (gdn_plan.cpp)
+int gdn_prefill_nv(int dv, int64_t pairs, int cu_count);
 // pieces the vocabulary of one sequence is cut into (gdn_plan.cpp)
 int accept_pieces(int64_t num_seqs, int64_t vocab, int cu_count);
 
 hipError_t launch_gdn_recurrent(const GdnRecurrentArgs& a, hipStream_t stream);
 hipError_t launch_gdn_sequential(const GdnPrefillArgs& a, const GdnTable& t, hipStream_t stream);
+hipError_t launch_gdn_chunked(const GdnPrefillArgs& a, const GdnTable& t, hipStream_t stream);
 hipError_t launch_accept(const AcceptArgs& a, hipStream_t stream);
 
 }  // namespace kda

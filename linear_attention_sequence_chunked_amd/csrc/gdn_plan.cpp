@@ -13,6 +13,14 @@ int gdn_recurrent_nv(int dv, int64_t pairs, int cu_count) {
     return pairs >= 2 * (int64_t)cu_count ? dv : 32;
 }
 
+int gdn_prefill_nv(int dv, int64_t pairs, int cu_count) {
+    // One workgroup runs per compute unit at a time (its LDS): the columns are split in halves
+    // until the (sequence, head) pairs cover every unit once, down to one 16-column block.
+    int nv = dv;
+    while (nv > 16 && pairs * (dv / nv) < cu_count) nv /= 2;
+    return nv;
+}
+
 int accept_pieces(int64_t num_seqs, int64_t vocab, int cu_count) {
     // Four workgroups per compute unit over the batch, but no piece below 2048 entries
     // (eight per thread) and at most 256 pieces (one partial sum per thread of the join).

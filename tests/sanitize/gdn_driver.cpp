@@ -19,6 +19,9 @@ hipError_t launch_gdn_sequential(const GdnPrefillArgs& a, const GdnTable& t, hip
     }
     return hipSuccess;
 }
+hipError_t launch_gdn_chunked(const GdnPrefillArgs& a, const GdnTable& t, hipStream_t s) {
+    return a.d.dv % a.nv ? hipErrorInvalidValue : launch_gdn_sequential(a, t, s);
+}
 hipError_t launch_gdn_recurrent(const GdnRecurrentArgs&, hipStream_t) { return hipErrorNotSupported; }
 hipError_t launch_accept(const AcceptArgs& a, hipStream_t) {
     return a.piece * a.pieces >= a.vocab && a.pieces <= 256 ? hipErrorNotSupported : hipSuccess;
