@@ -20,10 +20,11 @@
 // Sums of log-decays are fp64 (64 values per chunk and head: free) and kept as two floats, so
 // that G_t - G_s of near tokens keeps its accuracy behind a strong decay earlier in the chunk.
 //
-// Fragment conventions: kda_mfma.h.  Column order of the staged key and query rows, and of
-// every matrix that contracts over tokens: position 32p + 8g + 4h + i holds column
-// 32p + 16h + 4g + i, so one 16-byte read is the operand of a 32-deep step against two stacked
-// 16-row accumulator tiles.
+// Fragment conventions: kda_mfma.h.  A 32-deep operand holds eight consecutive key channels per
+// lane group, as they lie in memory: lane (r, g) of step p takes channels 32p + 8g .. +7.  The
+// state's accumulator tiles follow: tile 2p + h, row 4g + i is channel 32p + 8g + 4h + i.  Over
+// tokens (whose order the triangles fix) a step of 32 stacks two 16-row tiles instead: element
+// 4h + i of lane group g is token 16h + 4g + i of the 32.
 #pragma once
 
 #include "gdn_launch.h"
@@ -47,19 +48,11 @@ struct ValueTile {
     static constexpr int PPT = (PIECES + 255) / 256;
 };
 
-// byte of the 4-element group of columns 4c4 .. +3 in a permuted row
-__device__ __forceinline__ int perm4(int c4) { return 64 * (c4 >> 3) + 16 * (c4 & 3) + 8 * ((c4 >> 2) & 1); }
-
-// eight bf16 -> the two 8-byte groups of fp16 (or bf16 as they are)
+// eight bf16 -> eight fp16 (or bf16 as they are)
 template <bool HALF>
-__device__ __forceinline__ void groups8(u32x4 w, u32x2& a, u32x2& b) {
-    if constexpr (HALF) {
-        a = __builtin_bit_cast(u32x2, to_h4(unpack_bf4(u32x2{w[0], w[1]})));
-        b = __builtin_bit_cast(u32x2, to_h4(unpack_bf4(u32x2{w[2], w[3]})));
-    } else {
-        a = u32x2{w[0], w[1]};
-        b = u32x2{w[2], w[3]};
-    }
+__device__ __forceinline__ u32x4 staged8(u32x4 w) {
+    if constexpr (!HALF) return w;
+    return __builtin_bit_cast(u32x4, to_h8(unpack_bf4(u32x2{w[0], w[1]}), unpack_bf4(u32x2{w[2], w[3]})));
 }
 
 // Rows [0, rows) of a chunk of one head: 16-byte pieces, `pieces` per row, zeros behind the
@@ -75,16 +68,13 @@ __device__ __forceinline__ void load_rows(u32x4 (&dst)[PPT], const bf16* base, i
     }
 }
 
-// [64][DK] rows to LDS, columns permuted
+// [64][DK] rows to LDS
 template <int DK, bool HALF>
 __device__ __forceinline__ void store_key(unsigned char* tile, const u32x4 (&src)[KeyTile<DK>::PPT], int tid) {
 #pragma unroll
     for (int i = 0; i < KeyTile<DK>::PPT; ++i) {
-        const int e = tid + 256 * i, row = e / (DK / 8), m = e % (DK / 8);
-        u32x2 a, b;
-        groups8<HALF>(src[i], a, b);
-        lds_st(tile + row * KeyTile<DK>::RS + perm4(2 * m), a);
-        lds_st(tile + row * KeyTile<DK>::RS + perm4(2 * m + 1), b);
+        const int e = tid + 256 * i;
+        lds_st(tile + (e / (DK / 8)) * KeyTile<DK>::RS + (e % (DK / 8)) * 16, staged8<HALF>(src[i]));
     }
 }
 
@@ -109,70 +99,132 @@ __device__ __forceinline__ double wave_scan_f64(double x) {
 // it keep their accuracy and -inf - -inf does not arise; NaN stays.
 __device__ __forceinline__ double log2_decay(float la) { return (la < -1000.f ? -1000.0 : (double)la) * 1.4426950408889634074; }
 
-// Inverse of the unit lower triangular 16x16 block I + A by forward substitution: lane column
-// `col` of the block whose rows start at A (row stride 16 floats); x[i] = row i of that column.
-__device__ __forceinline__ void invert16(const float* A, int col, float (&x)[16]) {
+template <int J>
+__device__ __forceinline__ float row_bcast(float x) { return dpp<0x150 + J>(x); }  // lane J of the row of 16
+
+// Inverse of the unit lower triangular 16x16 blocks I + A by forward substitution, one block per
+// 16 lanes: lane c holds A's column c (a[i] = A[i][c]) and gets the inverse's column c.  The
+// element a step needs is in lane j of the row, where the FMA reads it in place (DPP).
+__device__ __forceinline__ void invert16(const float (&a)[16], int col, float (&x)[16]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float s = i == col ? 1.f : 0.f, s1 = 0.f;
+    for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.f : 0.f;
+    unroll<0, 15>([&](auto J) {
+        constexpr int j = decltype(J)::value;
 #pragma unroll
-        for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(A + 16 * i + 4 * j4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (4 * j4 + j < i) {
-                    if (j & 1) s1 = fmaf(-a[j], x[4 * j4 + j], s1);
-                    else s = fmaf(-a[j], x[4 * j4 + j], s);
-                }
-        }
-        x[i] = s + s1;
-    }
+        for (int i = j + 1; i < 16; ++i) x[i] = fmaf(-row_bcast<j>(a[i]), x[j], x[i]);
+    });
 }
 
-// LDS scratch of one half's inverse: A's two diagonal blocks and the block below them (fp32,
-// row-major), then the two inverses column by column.
+// LDS scratch of one half's inverse: two 16x16 blocks, column by column
 struct InvScratch {
-    static constexpr int BLK = 16 * 16 * 4 + 16;
-    static constexpr int DIAG = 0, SUB = 2 * BLK, COL = 3 * BLK, SIZE = 5 * BLK;
+    static constexpr int COL = 80;  // bytes of a column: 16 floats, padded
+    static constexpr int BLK = 16 * COL, SIZE = 2 * BLK;
 };
 
-// The 32x32 inverse of one half by one wave: rows[0] = row tile 0's columns 0..15, rows[1] and
-// rows[2] = row tile 1's columns 0..15 and 16..31; lane (r, g) gets row r, columns 4g .. 4g+3.
-__device__ __forceinline__ void invert32(unsigned char* sc, int lane, f32x4 (&rows)[3]) {
-    typedef InvScratch I;
-    const int r = lane & 15, g = lane >> 4, b = (lane >> 4) & 1;
-    float x[16];
-    invert16(reinterpret_cast<const float*>(sc + I::DIAG + b * I::BLK), r, x);
-    float* col = reinterpret_cast<float*>(sc + I::COL + b * I::BLK) + 16 * r;
-    if (lane < 32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<f32x4*>(col + 4 * i) = f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
-    }
+__device__ __forceinline__ void wave_lds_sync() {  // this wave's LDS writes before its reads
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
-    const float* ca = reinterpret_cast<const float*>(sc + I::COL);
-    const float* cb = reinterpret_cast<const float*>(sc + I::COL + I::BLK);
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// The 32x32 inverse of one half by one wave.  da, db: A's diagonal blocks (lane (r, g): rows
+// 4g .. 4g+3 of column r); sub: the block below them (lane (r, g): row r, columns 4g .. 4g+3).
+// rows[0]: row tile 0, columns 0..15; rows[1], rows[2]: row tile 1, columns 0..15 and 16..31;
+// lane (r, g) gets row r, columns 4g .. 4g+3.
+__device__ __forceinline__ void invert32(unsigned char* sc, int lane, f32x4 da, f32x4 db, f32x4 sub, f32x4 (&rows)[3]) {
+    typedef InvScratch I;
+    const int r = lane & 15, g = lane >> 4, b = g & 1;
+    lds_st(sc + I::COL * r + 16 * g, da);
+    lds_st(sc + I::BLK + I::COL * r + 16 * g, db);
+    wave_lds_sync();
+    float a[16], x[16];
+    unsigned char* mine = sc + b * I::BLK + I::COL * r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f32x4 v = lds_ld<f32x4>(mine + 16 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[4 * i + j] = v[j];
+    }
+    invert16(a, r, x);
+    if (lane < 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds_st(mine + 16 * i, f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
+    }
+    wave_lds_sync();
     f32x4 tb;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        rows[0][i] = ca[16 * (4 * g + i) + r];
-        tb[i] = cb[16 * (4 * g + i) + r];
+        rows[0][i] = lds_ld<float>(sc + I::COL * (4 * g + i) + 4 * r);
+        tb[i] = lds_ld<float>(sc + I::BLK + I::COL * (4 * g + i) + 4 * r);
     }
     // M = A_10 T_a, then the transpose of -T_b M (its accumulator is a row fragment)
-    const f32x4 sub = *reinterpret_cast<const f32x4*>(sc + I::SUB + 64 * r + 16 * g);
-    const f32x4 m = Mma<float>::run(sub, *reinterpret_cast<const f32x4*>(ca + 16 * r + 4 * g), zero4());
+    const f32x4 m = Mma<float>::run(sub, lds_ld<f32x4>(sc + I::COL * r + 16 * g), zero4());
     rows[1] = -Mma<float>::run(m, tb, zero4());
     rows[2] = tb;
 }
 
-// Tiles (it, jt), jt <= it, of the lower triangle of a 4x4 grid of 16x16 tiles, spread over the
-// four producer waves (3, 3, 2, 2 tiles)
-__device__ __forceinline__ int tri_tiles(int wave) { return wave < 2 ? 3 : 2; }
-__device__ __forceinline__ void tri_tile(int wave, int n, int& it, int& jt) {
-    const int idx = wave + 4 * n;  // 0..9: (0,0) (1,0) (1,1) (2,0) (2,1) (2,2) (3,0) ..
-    it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
-    jt = idx - it * (it + 1) / 2;
+// Decays and write strengths of the chunk's tokens in LDS: G (log2) as hi and lo floats, beta
+struct GateVec {
+    static constexpr int HI = 0, LO = 256, BE = 512, SIZE = 768;
+};
+
+// D_ts for one row t and the four columns s .. s+3, and for four rows and one column
+__device__ __forceinline__ f32x4 decay_row(const unsigned char* gv, int t, int s) {
+    const float th = lds_ld<float>(gv + GateVec::HI + 4 * t), tl = lds_ld<float>(gv + GateVec::LO + 4 * t);
+    const f32x4 sh = lds_ld<f32x4>(gv + GateVec::HI + 4 * s), sl = lds_ld<f32x4>(gv + GateVec::LO + 4 * s);
+    f32x4 d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = __builtin_amdgcn_exp2f((th - sh[i]) + (tl - sl[i]));
+    return d;
+}
+__device__ __forceinline__ f32x4 decay_col(const unsigned char* gv, int t, int s) {
+    const float sh = lds_ld<float>(gv + GateVec::HI + 4 * s), sl = lds_ld<float>(gv + GateVec::LO + 4 * s);
+    const f32x4 th = lds_ld<f32x4>(gv + GateVec::HI + 4 * t), tl = lds_ld<f32x4>(gv + GateVec::LO + 4 * t);
+    f32x4 d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = __builtin_amdgcn_exp2f((th[i] - sh) + (tl[i] - sl));
+    return d;
+}
+
+// Row fragments of one 16-token tile of a staged tensor, and the product of two of them:
+// lane (r, g) of tile_dot(X, Y) holds X_{4g+i} . Y_r
+template <int DK>
+struct TileRows {
+    f16x8 v[DK / 32];
+    __device__ __forceinline__ void load(const unsigned char* tile, int t, int r, int g) {
+#pragma unroll
+        for (int p = 0; p < DK / 32; ++p) v[p] = lds_ld<f16x8>(tile + (16 * t + r) * KeyTile<DK>::RS + 64 * p + 16 * g);
+    }
+};
+template <int DK>
+__device__ __forceinline__ f32x4 tile_dot(const TileRows<DK>& x, const TileRows<DK>& y) {
+    f32x4 c = zero4();
+#pragma unroll
+    for (int p = 0; p < DK / 32; ++p) c = mfma32h(x.v[p], y.v[p], c);
+    return c;
+}
+
+// A's three tiles of one half (rows and columns 32 half .. +31) and their inverse, by one wave
+template <int DK>
+__device__ __forceinline__ void half_inverse(const unsigned char* Kt, const unsigned char* gv, unsigned char* sc, int half,
+                                             int lane, f32x4 (&rows)[3]) {
+    const int r = lane & 15, g = lane >> 4, t0 = 32 * half;
+    TileRows<DK> k0, k1;
+    k0.load(Kt, 2 * half, r, g);
+    k1.load(Kt, 2 * half + 1, r, g);
+    f32x4 da = tile_dot<DK>(k0, k0), db = tile_dot<DK>(k1, k1), sub = tile_dot<DK>(k0, k1);
+    const f32x4 ba = lds_ld<f32x4>(gv + GateVec::BE + 4 * (t0 + 4 * g));
+    const f32x4 bb = lds_ld<f32x4>(gv + GateVec::BE + 4 * (t0 + 16 + 4 * g));
+    const float bs = lds_ld<float>(gv + GateVec::BE + 4 * (t0 + 16 + r));
+    const f32x4 ea = decay_col(gv, t0 + 4 * g, t0 + r), eb = decay_col(gv, t0 + 16 + 4 * g, t0 + 16 + r);
+    const f32x4 es = decay_row(gv, t0 + 16 + r, t0 + 4 * g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // selected, not multiplied: D above the diagonal may be inf
+        da[i] = 4 * g + i > r ? ba[i] * (ea[i] * da[i]) : 0.f;
+        db[i] = 4 * g + i > r ? bb[i] * (eb[i] * db[i]) : 0.f;
+        sub[i] = bs * (es[i] * sub[i]);
+    }
+    invert32(sc, lane, da, db, sub, rows);
 }
 
 }  // namespace kda

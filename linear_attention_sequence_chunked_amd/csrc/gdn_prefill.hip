@@ -12,8 +12,8 @@
 // registers: a chain wave takes only the key side from LDS and never waits for another chain
 // wave.  Four producer waves build the key side of chunk c+1 (gdn_chunk.h) while the chain
 // waves step chunk c; K, Q, V and the matrices are double-buffered in LDS, and the loads of
-// chunk c+2 are in flight meanwhile.  Three barriers per chunk order the producers among
-// themselves; the chain waves pass the same barriers where their own step allows.
+// chunk c+2 are in flight meanwhile.  Two of the producers form and invert A's diagonal halves,
+// each its own without a barrier between; the others form P and the block of A below.
 //
 // Precision.  Operands are fp16.  The products that make the state (K S, the solve, K^T U)
 // take their fp32 side as a pair hi + lo (22 bits): single operands would leave the fp32 state
@@ -47,8 +47,8 @@ struct GCfg {
     // vectors over the chunk's tokens: e^G, beta e^G, kPre beta, e^{G_C - G}; e^{G_C}
     static constexpr int V_EG = 0, V_BE = 256, V_B = 512, V_ER = 768, V_GC = 1024, V_SIZE = 1040;
     static constexpr int O_K = 0, O_Q = O_K + 2 * K::SIZE, O_V = O_Q + 2 * K::SIZE, O_M = O_V + 2 * V::SIZE,
-                         O_VEC = O_M + 2 * M_SIZE, O_G = O_VEC + 2 * V_SIZE,  // G hi, G lo, beta
-                         O_INV = O_G + 768, LDS_BYTES = O_INV + 2 * InvScratch::SIZE;
+                         O_VEC = O_M + 2 * M_SIZE, O_G = O_VEC + 2 * V_SIZE,
+                         O_INV = O_G + GateVec::SIZE, LDS_BYTES = O_INV + 2 * InvScratch::SIZE;
     static_assert(LDS_BYTES <= 160 * 1024, "LDS budget");
 };
 
@@ -129,7 +129,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
             }
         };
         if (nch > 0) load(0);
-        float* gh = reinterpret_cast<float*>(smem + C::O_G);
+        unsigned char* gv = smem + C::O_G;
         for (int c = 0; c <= nch; ++c) {  // builds chunk c; the last pass only keeps the barriers
             if (c < nch) {
                 unsigned char* Kt = buf(C::O_K, C::K::SIZE, c);
@@ -146,9 +146,9 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
                     const double G = wave_scan_f64(log2_decay(rla));
                     const double GC = __shfl(G, 63);
                     const float hi = (float)G, eg = __builtin_amdgcn_exp2f(hi);
-                    gh[lane] = hi;
-                    gh[64 + lane] = (float)(G - (double)hi);
-                    gh[128 + lane] = rbe;
+                    lds_st(gv + GateVec::HI + 4 * lane, hi);
+                    lds_st(gv + GateVec::LO + 4 * lane, (float)(G - (double)hi));
+                    lds_st(gv + GateVec::BE + 4 * lane, rbe);
                     float* vec = reinterpret_cast<float*>(buf(C::O_VEC, C::V_SIZE, c));
                     vec[C::V_EG / 4 + lane] = eg;
                     vec[C::V_BE / 4 + lane] = rbe * eg;
@@ -160,60 +160,58 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
             }
             lds_barrier();
             if (c < nch) {
-                // Gram tiles, transposed: lane (r, g) holds row 16 it + r, columns 16 jt + 4g ..
                 const unsigned char* Kt = buf(C::O_K, C::K::SIZE, c);
                 const unsigned char* Qt = buf(C::O_Q, C::K::SIZE, c);
                 unsigned char* M = buf(C::O_M, C::M_SIZE, c);
-                for (int n = 0; n < tri_tiles(pw); ++n) {
-                    int it, jt;
-                    tri_tile(pw, n, it, jt);
-                    f32x4 ka = zero4(), qa = zero4();
+                if (pw < 2) {
+                    f32x4 rows[3];
+                    half_inverse<DK>(Kt, gv, smem + C::O_INV + pw * InvScratch::SIZE, pw, lane, rows);
+                    unsigned char* d = M + (pw ? C::M_T1 : C::M_T0) + 16 * lane;
+                    const int at[3] = {0, C::FR, C::FR + 8};
 #pragma unroll
-                    for (int p = 0; p < C::KP; ++p) {
-                        const f16x8 kj = lds_ld<f16x8>(Kt + (16 * jt + r) * C::K::RS + 64 * p + 16 * g);
-                        const f16x8 ki = lds_ld<f16x8>(Kt + (16 * it + r) * C::K::RS + 64 * p + 16 * g);
-                        const f16x8 qi = lds_ld<f16x8>(Qt + (16 * it + r) * C::K::RS + 64 * p + 16 * g);
-                        ka = mfma32h(kj, ki, ka);
-                        qa = mfma32h(kj, qi, qa);
-                    }
-                    const float rh = gh[16 * it + r], rl = gh[64 + 16 * it + r], rb = gh[128 + 16 * it + r];
-                    const f32x4 ch = *reinterpret_cast<const f32x4*>(gh + 16 * jt + 4 * g);
-                    const f32x4 cl = *reinterpret_cast<const f32x4*>(gh + 64 + 16 * jt + 4 * g);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float d = __builtin_amdgcn_exp2f((rh - ch[i]) + (rl - cl[i]));
-                        const bool diag = it == jt;
-                        qa[i] = !diag || 4 * g + i <= r ? d * qa[i] : 0.f;
-                        ka[i] = !diag || 4 * g + i < r ? rb * (d * ka[i]) : 0.f;
-                    }
-                    // P: block (rows 32 (it / 2), columns 32 (jt / 2)), row tile it % 2
-                    const int pb = (it >> 1) + (jt >> 1);
-                    lds_st(M + C::M_P + (2 * pb + (it & 1)) * C::FR + 16 * lane + 8 * (jt & 1), to_h4(qa));
-                    if ((it >> 1) != (jt >> 1)) {
+                    for (int i = 0; i < 3; ++i) {
                         f16x4 hi, lo;
-                        split4h(-ka, hi, lo);
-                        unsigned char* d = M + C::M_A + (it & 1) * C::FR + 16 * lane + 8 * (jt & 1);
-                        lds_st(d, hi);
-                        lds_st(d + 2 * C::FR, lo);
-                    } else {
-                        unsigned char* sc = smem + C::O_INV + (it >> 1) * InvScratch::SIZE;
-                        const int at = it == jt ? InvScratch::DIAG + (it & 1) * InvScratch::BLK : InvScratch::SUB;
-                        lds_st(sc + at + 64 * r + 16 * g, ka);
+                        split4h(rows[i], hi, lo);
+                        lds_st(d + at[i], hi);
+                        lds_st(d + at[i] + 2 * C::FR, lo);
                     }
-                }
-            }
-            lds_barrier();
-            if (c < nch && pw < 2) {
-                unsigned char* M = buf(C::O_M, C::M_SIZE, c) + (pw ? C::M_T1 : C::M_T0);
-                f32x4 rows[3];
-                invert32(smem + C::O_INV + pw * InvScratch::SIZE, lane, rows);
-                const int at[3] = {0, C::FR, C::FR + 8};
+                } else {
+                    TileRows<DK> kt[4], qt;
+                    // P's tiles of row tile it, and -A's where they lie below the halves: lane
+                    // (r, g) holds row 16 it + r, columns 16 jt + 4g ..
+                    auto row_tiles = [&](auto IT) {
+                        constexpr int it = decltype(IT)::value;
+                        qt.load(Qt, it, r, g);
+                        unroll<0, it + 1>([&](auto JT) {
+                            constexpr int jt = decltype(JT)::value;
+                            const f32x4 d = decay_row(gv, 16 * it + r, 16 * jt + 4 * g);
+                            f32x4 p = tile_dot<DK>(kt[jt], qt);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    f16x4 hi, lo;
-                    split4h(rows[i], hi, lo);
-                    lds_st(M + at[i] + 16 * lane, hi);
-                    lds_st(M + at[i] + 2 * C::FR + 16 * lane, lo);
+                            for (int i = 0; i < 4; ++i) p[i] = it > jt || 4 * g + i <= r ? d[i] * p[i] : 0.f;
+                            // P: block (rows 32 (it / 2), columns 32 (jt / 2)), row tile it % 2
+                            lds_st(M + C::M_P + (2 * (it / 2 + jt / 2) + it % 2) * C::FR + 16 * lane + 8 * (jt % 2), to_h4(p));
+                            if constexpr (it / 2 != jt / 2) {
+                                const f32x4 x = tile_dot<DK>(kt[jt], kt[it]);
+                                const float nb = -lds_ld<float>(gv + GateVec::BE + 4 * (16 * it + r));
+                                f16x4 hi, lo;
+                                split4h(nb * (d * x), hi, lo);
+                                unsigned char* m = M + C::M_A + (it % 2) * C::FR + 16 * lane + 8 * (jt % 2);
+                                lds_st(m, hi);
+                                lds_st(m + 2 * C::FR, lo);
+                            }
+                        });
+                    };
+                    kt[0].load(Kt, 0, r, g);
+                    kt[1].load(Kt, 1, r, g);
+                    kt[2].load(Kt, 2, r, g);
+                    if (pw == 2) {
+                        row_tiles(std::integral_constant<int, 2>{});
+                        row_tiles(std::integral_constant<int, 1>{});
+                        row_tiles(std::integral_constant<int, 0>{});
+                    } else {
+                        kt[3].load(Kt, 3, r, g);
+                        row_tiles(std::integral_constant<int, 3>{});
+                    }
                 }
             }
             lds_barrier();
@@ -225,6 +223,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
     constexpr int KB = C::KB, KP = C::KP, CPW = C::CPW;
     f32x4 S[CPW][KB];
     int ccol[CPW];
+    auto channel = [&](int b) { return 32 * (b >> 1) + 8 * g + 4 * (b & 1); };  // of a tile's first row
 #pragma unroll
     for (int cb = 0; cb < CPW; ++cb) {
         ccol[cb] = col0 + 16 * (CPW * wave + cb) + r;
@@ -232,7 +231,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                S[cb][b][i] = a.S0 ? kPre * a.S0[sbase + (int64_t)(16 * b + 4 * g + i) * a.dv + ccol[cb]] : 0.f;
+                S[cb][b][i] = a.S0 ? kPre * a.S0[sbase + (int64_t)(channel(b) + i) * a.dv + ccol[cb]] : 0.f;
     }
     const int trj = (lane & 15) >> 2, trq = lane & 3;
     const int tr_k = (4 * g + trj) * C::K::RS + 16 * trq;
@@ -242,7 +241,6 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
     const int64_t os = (int64_t)a.hv * a.dv;
 
     lds_barrier();  // chunk 0 is built in the producers' first pass
-    lds_barrier();
     lds_barrier();
     for (int c = 0; c < nch; ++c) {
         const unsigned char* Kt = buf(C::O_K, C::K::SIZE, c);
@@ -274,7 +272,6 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
                 }
             }
         }
-        lds_barrier();
         // X = kPre beta V - beta e^G Y, in place of Y
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -367,7 +364,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
             for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    a.Sf[sbase + (int64_t)(16 * b + 4 * g + i) * a.dv + ccol[cb]] = S[cb][b][i] * (1.f / kPre);
+                    a.Sf[sbase + (int64_t)(channel(b) + i) * a.dv + ccol[cb]] = S[cb][b][i] * (1.f / kPre);
     }
 }
 
