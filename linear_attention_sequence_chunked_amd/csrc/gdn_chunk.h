@@ -127,42 +127,6 @@ __device__ __forceinline__ void wave_lds_sync() {  // this wave's LDS writes bef
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
-// The 32x32 inverse of one half by one wave.  da, db: A's diagonal blocks (lane (r, g): rows
-// 4g .. 4g+3 of column r); sub: the block below them (lane (r, g): row r, columns 4g .. 4g+3).
-// rows[0]: row tile 0, columns 0..15; rows[1], rows[2]: row tile 1, columns 0..15 and 16..31;
-// lane (r, g) gets row r, columns 4g .. 4g+3.
-__device__ __forceinline__ void invert32(unsigned char* sc, int lane, f32x4 da, f32x4 db, f32x4 sub, f32x4 (&rows)[3]) {
-    typedef InvScratch I;
-    const int r = lane & 15, g = lane >> 4, b = g & 1;
-    lds_st(sc + I::COL * r + 16 * g, da);
-    lds_st(sc + I::BLK + I::COL * r + 16 * g, db);
-    wave_lds_sync();
-    float a[16], x[16];
-    unsigned char* mine = sc + b * I::BLK + I::COL * r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const f32x4 v = lds_ld<f32x4>(mine + 16 * i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[4 * i + j] = v[j];
-    }
-    invert16(a, r, x);
-    if (lane < 32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lds_st(mine + 16 * i, f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
-    }
-    wave_lds_sync();
-    f32x4 tb;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        rows[0][i] = lds_ld<float>(sc + I::COL * (4 * g + i) + 4 * r);
-        tb[i] = lds_ld<float>(sc + I::BLK + I::COL * (4 * g + i) + 4 * r);
-    }
-    // M = A_10 T_a, then the transpose of -T_b M (its accumulator is a row fragment)
-    const f32x4 m = Mma<float>::run(sub, lds_ld<f32x4>(sc + I::COL * r + 16 * g), zero4());
-    rows[1] = -Mma<float>::run(m, tb, zero4());
-    rows[2] = tb;
-}
-
 // Decays and write strengths of the chunk's tokens in LDS: G (log2) as hi and lo floats, beta
 struct GateVec {
     static constexpr int HI = 0, LO = 256, BE = 512, SIZE = 768;
@@ -204,10 +168,13 @@ __device__ __forceinline__ f32x4 tile_dot(const TileRows<DK>& x, const TileRows<
     return c;
 }
 
-// A's three tiles of one half (rows and columns 32 half .. +31) and their inverse, by one wave
+// The 32x32 inverse of one half (rows and columns 32 half .. +31 of A) by one wave, in two
+// steps that a barrier may separate.  First A's tiles and the inverses of its diagonal blocks,
+// column by column into the scratch; `sub` is the block below them, lane (r, g): row r,
+// columns 4g .. 4g+3.
 template <int DK>
-__device__ __forceinline__ void half_inverse(const unsigned char* Kt, const unsigned char* gv, unsigned char* sc, int half,
-                                             int lane, f32x4 (&rows)[3]) {
+__device__ __forceinline__ f32x4 half_columns(const unsigned char* Kt, const unsigned char* gv, unsigned char* sc, int half, int lane) {
+    typedef InvScratch I;
     const int r = lane & 15, g = lane >> 4, t0 = 32 * half;
     TileRows<DK> k0, k1;
     k0.load(Kt, 2 * half, r, g);
@@ -224,7 +191,40 @@ __device__ __forceinline__ void half_inverse(const unsigned char* Kt, const unsi
         db[i] = 4 * g + i > r ? bb[i] * (eb[i] * db[i]) : 0.f;
         sub[i] = bs * (es[i] * sub[i]);
     }
-    invert32(sc, lane, da, db, sub, rows);
+    lds_st(sc + I::COL * r + 16 * g, da);
+    lds_st(sc + I::BLK + I::COL * r + 16 * g, db);
+    wave_lds_sync();
+    float a[16], x[16];
+    unsigned char* mine = sc + (g & 1) * I::BLK + I::COL * r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f32x4 v = lds_ld<f32x4>(mine + 16 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[4 * i + j] = v[j];
+    }
+    invert16(a, r, x);
+    if (lane < 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds_st(mine + 16 * i, f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
+    }
+    wave_lds_sync();
+    return sub;
+}
+// Then the join.  rows[0]: row tile 0, columns 0..15; rows[1], rows[2]: row tile 1, columns
+// 0..15 and 16..31; lane (r, g) gets row r, columns 4g .. 4g+3.
+__device__ __forceinline__ void half_join(const unsigned char* sc, f32x4 sub, int lane, f32x4 (&rows)[3]) {
+    typedef InvScratch I;
+    const int r = lane & 15, g = lane >> 4;
+    f32x4 tb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        rows[0][i] = lds_ld<float>(sc + I::COL * (4 * g + i) + 4 * r);
+        tb[i] = lds_ld<float>(sc + I::BLK + I::COL * (4 * g + i) + 4 * r);
+    }
+    // M = A_10 T_a, then the transpose of -T_b M (its accumulator is a row fragment)
+    const f32x4 m = Mma<float>::run(sub, lds_ld<f32x4>(sc + I::COL * r + 16 * g), zero4());
+    rows[1] = -Mma<float>::run(m, tb, zero4());
+    rows[2] = tb;
 }
 
 }  // namespace kda

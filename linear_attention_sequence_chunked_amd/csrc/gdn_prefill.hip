@@ -10,10 +10,23 @@
 // sequence.  An accumulator tile is, register for register, the B operand (and, transposed,
 // the A operand) of the next product over the same rows, so S, X and U never leave the
 // registers: a chain wave takes only the key side from LDS and never waits for another chain
-// wave.  Four producer waves build the key side of chunk c+1 (gdn_chunk.h) while the chain
-// waves step chunk c; K, Q, V and the matrices are double-buffered in LDS, and the loads of
-// chunk c+2 are in flight meanwhile.  Two of the producers form and invert A's diagonal halves,
-// each its own without a barrier between; the others form P and the block of A below.
+// wave.  The key side of the chunks to come is built by other waves meanwhile (gdn_chunk.h).
+//
+// The loop's passes have two phases, each ended by a workgroup barrier (LDS only: loads and
+// stores stay in flight).  Pass c:
+//              phase A                             phase B
+//   stage      K, Q, V, decays of chunk c          (loads of c+1 in flight)
+//   inverse    (I + A)'s halves: join of c-1       tiles and substitution of c
+//   gram       P of c-1, lower rows                P of c, upper rows; A below the halves
+//   chain      K S of c-1                          X, U of c-1, the state behind it
+//   out        P U of c-2, its rows stored         Q S of c-1
+// K, Q, V, the decays and the matrices are double-buffered; S and U reach the out wave as the
+// fp16 operands they are, through LDS.  Two forms:
+//  * narrow (16 or 32 columns, few chains: the step's latency is the launch's time): every row
+//    above has waves of its own (4, 2, 2, one per 16 columns, 1);
+//  * wide (64 or 128 columns): the chain waves (two column blocks each at 128) do the out
+//    wave's work on their own registers, and four producer waves stage in phase A and invert
+//    or form Gram tiles, two and two, in phase B; more waves would not have the registers.
 //
 // Precision.  Operands are fp16.  The products that make the state (K S, the solve, K^T U)
 // take their fp32 side as a pair hi + lo (22 bits): single operands would leave the fp32 state
@@ -33,11 +46,14 @@ constexpr float kPre = 8.f;  // v and the state are carried times this
 template <int DK, int NCB>
 struct GCfg {
     static constexpr int KB = DK / 16, KP = DK / 32, NV = 16 * NCB;
+    static constexpr bool NARROW = NCB <= 2;
     // two column blocks per chain wave at full width, so that an operand read from LDS serves
     // 32 columns; one otherwise (the shortest step)
     static constexpr int CPW = NCB >= 8 ? 2 : 1;
     static constexpr int NCHAIN = NCB / CPW;
-    static constexpr int THREADS = 64 * (NCHAIN + 4);
+    // wave numbers: chain, stage (the wide form's producers), inverse, gram, out
+    static constexpr int W_STAGE = NCHAIN, W_INV = NARROW ? W_STAGE + 4 : W_STAGE, W_GRAM = W_INV + 2,
+                         W_OUT = W_GRAM + 2, WAVES = W_OUT + (NARROW ? 1 : 0), THREADS = 64 * WAVES;
     typedef KeyTile<DK> K;
     typedef ValueTile<NV> V;
     // matrices, as operand fragments (16 bytes per lane): row tiles 0 and 1 of T's upper half,
@@ -46,9 +62,11 @@ struct GCfg {
     static constexpr int M_T0 = 0, M_T1 = 4 * FR, M_A = 8 * FR, M_P = 12 * FR, M_SIZE = 18 * FR;
     // vectors over the chunk's tokens: e^G, beta e^G, kPre beta, e^{G_C - G}; e^{G_C}
     static constexpr int V_EG = 0, V_BE = 256, V_B = 512, V_ER = 768, V_GC = 1024, V_SIZE = 1040;
+    // operands for the out wave, per column block: S, then U
+    static constexpr int X_S = 0, X_U = KP * FR, X_SIZE = X_U + 2 * FR;
     static constexpr int O_K = 0, O_Q = O_K + 2 * K::SIZE, O_V = O_Q + 2 * K::SIZE, O_M = O_V + 2 * V::SIZE,
-                         O_VEC = O_M + 2 * M_SIZE, O_G = O_VEC + 2 * V_SIZE,
-                         O_INV = O_G + GateVec::SIZE, LDS_BYTES = O_INV + 2 * InvScratch::SIZE;
+                         O_VEC = O_M + 2 * M_SIZE, O_G = O_VEC + 2 * V_SIZE, O_INV = O_G + 2 * GateVec::SIZE,
+                         O_X = O_INV + 2 * InvScratch::SIZE, LDS_BYTES = O_X + (NARROW ? NCB * X_SIZE : 0);
     static_assert(LDS_BYTES <= 160 * 1024, "LDS budget");
 };
 
@@ -106,121 +124,226 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         lds_st(smem + C::O_M + 16 * i, u32x4{0u, 0u, 0u, 0u});
     lds_barrier();
 
-    if (wave >= C::NCHAIN) {
-        // ================================================================ producers
-        const int pw = wave - C::NCHAIN, pt = tid - 64 * C::NCHAIN;
-        u32x4 rk[C::K::PPT], rq[C::K::PPT], rv[C::V::PPT];
-        float rla = 0.f, rbe = 0.f;
-        const bf16* pq = a.q + start * a.qs + (int64_t)hk * DK;
-        const bf16* pk = a.k + start * a.ks + (int64_t)hk * DK;
-        const bf16* pv = a.v + start * a.vs + (int64_t)h * a.dv + col0;
-        auto load = [&](int c) {
-            const int rows = min(kGC, len - kGC * c);
-            const int64_t at = (int64_t)kGC * c;
-            load_rows<C::K::PPT, DK / 8>(rk, pk + at * a.ks, a.ks, rows, pt);
-            load_rows<C::K::PPT, DK / 8>(rq, pq + at * a.qs, a.qs, rows, pt);
-            load_rows<C::V::PPT, C::NV / 8>(rv, pv + at * a.vs, a.vs, rows, pt);
-            if (pw == 0) {
-                rla = rbe = 0.f;
-                if (lane < rows) {
-                    rla = a.la[(start + at + lane) * a.hv + h];
-                    rbe = a.be[(start + at + lane) * a.hv + h];
-                }
-            }
-        };
-        if (nch > 0) load(0);
-        unsigned char* gv = smem + C::O_G;
-        for (int c = 0; c <= nch; ++c) {  // builds chunk c; the last pass only keeps the barriers
-            if (c < nch) {
-                unsigned char* Kt = buf(C::O_K, C::K::SIZE, c);
-                unsigned char* Qt = buf(C::O_Q, C::K::SIZE, c);
-                unsigned char* Vt = buf(C::O_V, C::V::SIZE, c);
-                store_key<DK, true>(Kt, rk, pt);
-                store_key<DK, true>(Qt, rq, pt);
+    constexpr int KB = C::KB, KP = C::KP, CPW = C::CPW;
+    const float oscale = a.scale / kPre;
+    const int64_t os = (int64_t)a.hv * a.dv;
+    bf16* po = a.out + start * os + (int64_t)h * a.dv + col0 + 4 * g;
+
+    // ------------------------------------------------------------------ parts of the key side
+    struct Staged {
+        u32x4 k[C::K::PPT], q[C::K::PPT], v[C::V::PPT];
+        float la, be;
+    };
+    const int st = tid - 64 * C::W_STAGE;  // thread among the staging waves
+    auto load = [&](Staged& x, int c) {
+        const int rows = min(kGC, len - kGC * c);
+        const int64_t at = start + (int64_t)kGC * c;
+        load_rows<C::K::PPT, DK / 8>(x.k, a.k + at * a.ks + (int64_t)hk * DK, a.ks, rows, st);
+        load_rows<C::K::PPT, DK / 8>(x.q, a.q + at * a.qs + (int64_t)hk * DK, a.qs, rows, st);
+        load_rows<C::V::PPT, C::NV / 8>(x.v, a.v + at * a.vs + (int64_t)h * a.dv + col0, a.vs, rows, st);
+        x.la = x.be = 0.f;
+        if (wave == C::W_STAGE && lane < rows) {
+            x.la = a.la[(at + lane) * a.hv + h];
+            x.be = a.be[(at + lane) * a.hv + h];
+        }
+    };
+    auto stage = [&](const Staged& x, int c) {
+        unsigned char* Vt = buf(C::O_V, C::V::SIZE, c);
+        store_key<DK, true>(buf(C::O_K, C::K::SIZE, c), x.k, st);
+        store_key<DK, true>(buf(C::O_Q, C::K::SIZE, c), x.q, st);
 #pragma unroll
-                for (int i = 0; i < C::V::PPT; ++i) {
-                    const int e = pt + 256 * i;
-                    if (e < C::V::PIECES) lds_st(Vt + (e / (C::NV / 8)) * C::V::RS + (e % (C::NV / 8)) * 16, rv[i]);
-                }
-                if (pw == 0) {
-                    const double G = wave_scan_f64(log2_decay(rla));
-                    const double GC = __shfl(G, 63);
-                    const float hi = (float)G, eg = __builtin_amdgcn_exp2f(hi);
-                    lds_st(gv + GateVec::HI + 4 * lane, hi);
-                    lds_st(gv + GateVec::LO + 4 * lane, (float)(G - (double)hi));
-                    lds_st(gv + GateVec::BE + 4 * lane, rbe);
-                    float* vec = reinterpret_cast<float*>(buf(C::O_VEC, C::V_SIZE, c));
-                    vec[C::V_EG / 4 + lane] = eg;
-                    vec[C::V_BE / 4 + lane] = rbe * eg;
-                    vec[C::V_B / 4 + lane] = kPre * rbe;
-                    vec[C::V_ER / 4 + lane] = __builtin_amdgcn_exp2f((float)(GC - G));
-                    if (lane == 0) vec[C::V_GC / 4] = __builtin_amdgcn_exp2f((float)GC);
-                }
-                if (c + 1 < nch) load(c + 1);
+        for (int i = 0; i < C::V::PPT; ++i) {
+            const int e = st + 256 * i;
+            if (e < C::V::PIECES) lds_st(Vt + (e / (C::NV / 8)) * C::V::RS + (e % (C::NV / 8)) * 16, x.v[i]);
+        }
+        if (wave == C::W_STAGE) {
+            const double G = wave_scan_f64(log2_decay(x.la)), GC = __shfl(G, 63);
+            const float hi = (float)G, eg = __builtin_amdgcn_exp2f(hi);
+            unsigned char* gv = buf(C::O_G, GateVec::SIZE, c);
+            lds_st(gv + GateVec::HI + 4 * lane, hi);
+            lds_st(gv + GateVec::LO + 4 * lane, (float)(G - (double)hi));
+            lds_st(gv + GateVec::BE + 4 * lane, x.be);
+            unsigned char* vec = buf(C::O_VEC, C::V_SIZE, c);
+            lds_st(vec + C::V_EG + 4 * lane, eg);
+            lds_st(vec + C::V_BE + 4 * lane, x.be * eg);
+            lds_st(vec + C::V_B + 4 * lane, kPre * x.be);
+            lds_st(vec + C::V_ER + 4 * lane, __builtin_amdgcn_exp2f((float)(GC - G)));
+            if (lane == 0) lds_st(vec + C::V_GC, __builtin_amdgcn_exp2f((float)GC));
+        }
+    };
+    unsigned char* isc = smem + C::O_INV + (wave - C::W_INV) * InvScratch::SIZE;  // inverse waves
+    auto columns = [&](int c) {
+        return half_columns<DK>(buf(C::O_K, C::K::SIZE, c), buf(C::O_G, GateVec::SIZE, c), isc, wave - C::W_INV, lane);
+    };
+    auto join = [&](f32x4 sub, int c) {
+        f32x4 rows[3];
+        half_join(isc, sub, lane, rows);
+        unsigned char* d = buf(C::O_M, C::M_SIZE, c) + (wave == C::W_INV ? C::M_T0 : C::M_T1) + 16 * lane;
+        const int at[3] = {0, C::FR, C::FR + 8};
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            f16x4 hi, lo;
+            split4h(rows[i], hi, lo);
+            lds_st(d + at[i], hi);
+            lds_st(d + at[i] + 2 * C::FR, lo);
+        }
+    };
+    // P's tiles of row tile it from column tile J0 on, and -A's where they lie below the halves:
+    // lane (r, g) holds row 16 it + r, columns 16 jt + 4g ..
+    auto gram_row = [&](auto IT, auto J0, int c) {
+        constexpr int it = decltype(IT)::value;
+        const unsigned char* Kt = buf(C::O_K, C::K::SIZE, c);
+        const unsigned char* gv = buf(C::O_G, GateVec::SIZE, c);
+        unsigned char* M = buf(C::O_M, C::M_SIZE, c);
+        TileRows<DK> qt, ki;
+        qt.load(buf(C::O_Q, C::K::SIZE, c), it, r, g);
+        if constexpr (it >= 2) ki.load(Kt, it, r, g);
+        unroll<decltype(J0)::value, it + 1>([&](auto JT) {
+            constexpr int jt = decltype(JT)::value;
+            TileRows<DK> kj;
+            kj.load(Kt, jt, r, g);
+            const f32x4 d = decay_row(gv, 16 * it + r, 16 * jt + 4 * g);
+            f32x4 p = tile_dot<DK>(kj, qt);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = it > jt || 4 * g + i <= r ? d[i] * p[i] : 0.f;
+            // P: block (rows 32 (it / 2), columns 32 (jt / 2)), row tile it % 2
+            lds_st(M + C::M_P + (2 * (it / 2 + jt / 2) + it % 2) * C::FR + 16 * lane + 8 * (jt % 2), to_h4(p));
+            if constexpr (it / 2 != jt / 2) {
+                const f32x4 x = tile_dot<DK>(kj, ki);
+                const float nb = -lds_ld<float>(gv + GateVec::BE + 4 * (16 * it + r));
+                f16x4 hi, lo;
+                split4h(nb * (d * x), hi, lo);
+                unsigned char* m = M + C::M_A + (it % 2) * C::FR + 16 * lane + 8 * (jt % 2);
+                lds_st(m, hi);
+                lds_st(m + 2 * C::FR, lo);
+            }
+        });
+    };
+    using std::integral_constant;
+    constexpr integral_constant<int, 0> i0;
+    constexpr integral_constant<int, 1> i1;
+    constexpr integral_constant<int, 2> i2;
+    constexpr integral_constant<int, 3> i3;
+    // one chunk's Gram work of gram wave n, first and second part
+    auto gram_first = [&](int n, int c) {
+        if (n == 0) gram_row(i2, i0, c);
+        else gram_row(i3, i0, c);
+    };
+    auto gram_second = [&](int n, int c) {
+        if (n == 0) {
+            gram_row(i1, i0, c);
+            gram_row(i0, i0, c);
+        }
+    };
+
+    if (!C::NARROW && wave >= C::W_STAGE) {
+        // ---------------------------------------------------------------- wide: producers
+        Staged x;
+        if (nch > 0) load(x, 0);
+        for (int c = 0; c <= nch; ++c) {
+            if (c < nch) {
+                stage(x, c);
+                if (c + 1 < nch) load(x, c + 1);
             }
             lds_barrier();
             if (c < nch) {
-                const unsigned char* Kt = buf(C::O_K, C::K::SIZE, c);
-                const unsigned char* Qt = buf(C::O_Q, C::K::SIZE, c);
-                unsigned char* M = buf(C::O_M, C::M_SIZE, c);
-                if (pw < 2) {
-                    f32x4 rows[3];
-                    half_inverse<DK>(Kt, gv, smem + C::O_INV + pw * InvScratch::SIZE, pw, lane, rows);
-                    unsigned char* d = M + (pw ? C::M_T1 : C::M_T0) + 16 * lane;
-                    const int at[3] = {0, C::FR, C::FR + 8};
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        f16x4 hi, lo;
-                        split4h(rows[i], hi, lo);
-                        lds_st(d + at[i], hi);
-                        lds_st(d + at[i] + 2 * C::FR, lo);
-                    }
+                if (wave < C::W_GRAM) {
+                    join(columns(c), c);
                 } else {
-                    TileRows<DK> kt[4], qt;
-                    // P's tiles of row tile it, and -A's where they lie below the halves: lane
-                    // (r, g) holds row 16 it + r, columns 16 jt + 4g ..
-                    auto row_tiles = [&](auto IT) {
-                        constexpr int it = decltype(IT)::value;
-                        qt.load(Qt, it, r, g);
-                        unroll<0, it + 1>([&](auto JT) {
-                            constexpr int jt = decltype(JT)::value;
-                            const f32x4 d = decay_row(gv, 16 * it + r, 16 * jt + 4 * g);
-                            f32x4 p = tile_dot<DK>(kt[jt], qt);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) p[i] = it > jt || 4 * g + i <= r ? d[i] * p[i] : 0.f;
-                            // P: block (rows 32 (it / 2), columns 32 (jt / 2)), row tile it % 2
-                            lds_st(M + C::M_P + (2 * (it / 2 + jt / 2) + it % 2) * C::FR + 16 * lane + 8 * (jt % 2), to_h4(p));
-                            if constexpr (it / 2 != jt / 2) {
-                                const f32x4 x = tile_dot<DK>(kt[jt], kt[it]);
-                                const float nb = -lds_ld<float>(gv + GateVec::BE + 4 * (16 * it + r));
-                                f16x4 hi, lo;
-                                split4h(nb * (d * x), hi, lo);
-                                unsigned char* m = M + C::M_A + (it % 2) * C::FR + 16 * lane + 8 * (jt % 2);
-                                lds_st(m, hi);
-                                lds_st(m + 2 * C::FR, lo);
-                            }
-                        });
-                    };
-                    kt[0].load(Kt, 0, r, g);
-                    kt[1].load(Kt, 1, r, g);
-                    kt[2].load(Kt, 2, r, g);
-                    if (pw == 2) {
-                        row_tiles(std::integral_constant<int, 2>{});
-                        row_tiles(std::integral_constant<int, 1>{});
-                        row_tiles(std::integral_constant<int, 0>{});
-                    } else {
-                        kt[3].load(Kt, 3, r, g);
-                        row_tiles(std::integral_constant<int, 3>{});
-                    }
+                    gram_first(wave - C::W_GRAM, c);
+                    gram_second(wave - C::W_GRAM, c);
                 }
             }
             lds_barrier();
         }
         return;
     }
+    if (C::NARROW && wave >= C::W_STAGE && wave < C::W_INV) {
+        Staged x;
+        if (nch > 0) load(x, 0);
+        for (int c = 0; c <= nch; ++c) {
+            if (c < nch) stage(x, c);
+            if (c + 1 < nch) load(x, c + 1);
+            lds_barrier();
+            lds_barrier();
+        }
+        return;
+    }
+    if (C::NARROW && wave >= C::W_INV && wave < C::W_GRAM) {
+        f32x4 sub = zero4();
+        for (int c = 0; c <= nch; ++c) {
+            if (c > 0) join(sub, c - 1);
+            lds_barrier();
+            if (c < nch) sub = columns(c);
+            lds_barrier();
+        }
+        return;
+    }
+    if (C::NARROW && wave >= C::W_GRAM && wave < C::W_OUT) {
+        for (int c = 0; c <= nch; ++c) {
+            if (c > 0) gram_second(wave - C::W_GRAM, c - 1);
+            lds_barrier();
+            if (c < nch) gram_first(wave - C::W_GRAM, c);
+            lds_barrier();
+        }
+        return;
+    }
+    // rows of O^T + (P U)^T of chunk c, scaled and stored: lane (r, g) holds token r of the
+    // tile, columns 4g .. 4g+3
+    auto finish = [&](f32x4 o, f16x8 u0, f16x8 u1, auto T, int c, int col) {
+        constexpr int t = decltype(T)::value;
+        const unsigned char* P = buf(C::O_M, C::M_SIZE, c) + C::M_P + 16 * lane;
+        o = mfma32h(u0, lds_ld<f16x8>(P + t * C::FR), o);
+        if constexpr (t >= 2) o = mfma32h(u1, lds_ld<f16x8>(P + (2 + t) * C::FR), o);
+        const int row = kGC * c + 16 * t + r;
+        if (row < len) *reinterpret_cast<bf16x4*>(po + (int64_t)row * os + col) = to_bf4(oscale * o);
+    };
+    if (C::NARROW && wave == C::W_OUT) {
+        f32x4 O[NCB][4];
+        auto done = [&](int c) {
+#pragma unroll
+            for (int cb = 0; cb < NCB; ++cb) {
+                const unsigned char* x = smem + C::O_X + cb * C::X_SIZE + C::X_U + 16 * lane;
+                const f16x8 u0 = lds_ld<f16x8>(x), u1 = lds_ld<f16x8>(x + C::FR);
+                unroll<0, 4>([&](auto T) { finish(O[cb][decltype(T)::value], u0, u1, T, c, 16 * cb); });
+            }
+        };
+        for (int c = 0; c <= nch; ++c) {
+            if (c > 1) done(c - 2);
+            lds_barrier();
+            if (c > 0) {
+                const unsigned char* Qt = buf(C::O_Q, C::K::SIZE, c - 1);
+                const unsigned char* vec = buf(C::O_VEC, C::V_SIZE, c - 1);
+#pragma unroll
+                for (int cb = 0; cb < NCB; ++cb)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) O[cb][t] = zero4();
+#pragma unroll
+                for (int p = 0; p < KP; ++p) {
+                    f16x8 sh[NCB];
+#pragma unroll
+                    for (int cb = 0; cb < NCB; ++cb) sh[cb] = lds_ld<f16x8>(smem + C::O_X + cb * C::X_SIZE + p * C::FR + 16 * lane);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const f16x8 qf = lds_ld<f16x8>(Qt + (16 * t + r) * C::K::RS + 64 * p + 16 * g);
+#pragma unroll
+                        for (int cb = 0; cb < NCB; ++cb) O[cb][t] = mfma32h(sh[cb], qf, O[cb][t]);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const float eg = lds_ld<float>(vec + C::V_EG + 4 * (16 * t + r));
+#pragma unroll
+                    for (int cb = 0; cb < NCB; ++cb) O[cb][t] *= eg;
+                }
+            }
+            lds_barrier();
+        }
+        if (nch > 0) done(nch - 1);
+        return;
+    }
 
     // ==================================================================== chain waves
-    constexpr int KB = C::KB, KP = C::KP, CPW = C::CPW;
     f32x4 S[CPW][KB];
     int ccol[CPW];
     auto channel = [&](int b) { return 32 * (b >> 1) + 8 * g + 4 * (b & 1); };  // of a tile's first row
@@ -236,124 +359,208 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
     const int trj = (lane & 15) >> 2, trq = lane & 3;
     const int tr_k = (4 * g + trj) * C::K::RS + 16 * trq;
     const int tr_v = (4 * g + trj) * C::V::RS + 8 * trq;
-    const float oscale = a.scale / kPre;
-    bf16* po = a.out + start * a.hv * a.dv + (int64_t)h * a.dv + col0 + 16 * CPW * wave + 4 * g;
-    const int64_t os = (int64_t)a.hv * a.dv;
+    unsigned char* xw = smem + C::O_X + wave * C::X_SIZE + 16 * lane;  // narrow: to the out wave
 
-    lds_barrier();  // chunk 0 is built in the producers' first pass
+    // Rows of K (and Q) of step p as operands.  They are read a step ahead, the
+    // first before the barrier that starts the chunk's step (they were staged a phase earlier),
+    // so LDS latency stays off the chain.
+    typedef f16x8 Rows[4];
+    auto load_k = [&](Rows& x, int c, int p) {
+        const unsigned char* at = buf(C::O_K, C::K::SIZE, c) + r * C::K::RS + 64 * p + 16 * g;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) x[t] = lds_ld<f16x8>(at + 16 * t * C::K::RS);
+    };
+    auto load_q = [&](Rows& x, int c, int p) {
+        const unsigned char* at = buf(C::O_Q, C::K::SIZE, c) + r * C::K::RS + 64 * p + 16 * g;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) x[t] = lds_ld<f16x8>(at + 16 * t * C::K::RS);
+    };
+    Rows kf[2], qf[2];
+
+    __builtin_amdgcn_s_setprio(3);  // the chain's instructions before the others' on its SIMD
+    lds_barrier();  // pass 0: chunk 0 is staged
+    if (nch > 0) {
+        load_k(kf[0], 0, 0);
+        if constexpr (!C::NARROW) load_q(qf[0], 0, 0);
+    }
     lds_barrier();
     for (int c = 0; c < nch; ++c) {
         const unsigned char* Kt = buf(C::O_K, C::K::SIZE, c);
-        const unsigned char* Qt = buf(C::O_Q, C::K::SIZE, c);
         const unsigned char* Vt = buf(C::O_V, C::V::SIZE, c);
         const unsigned char* M = buf(C::O_M, C::M_SIZE, c);
-        const float* vec = reinterpret_cast<const float*>(buf(C::O_VEC, C::V_SIZE, c));
+        const unsigned char* vec = buf(C::O_VEC, C::V_SIZE, c);
         auto frag = [&](int off) { return lds_ld<f16x8>(M + off + 16 * lane); };
+        auto tokens = [&](int v, int t) { return lds_ld<f32x4>(vec + v + 4 * (t + 4 * g)); };
         // Y = K S (rows of tokens) and (Q S)^T (rows of value columns)
         f32x4 Y[CPW][4], O[CPW][4];
 #pragma unroll
         for (int cb = 0; cb < CPW; ++cb)
 #pragma unroll
             for (int t = 0; t < 4; ++t) Y[cb][t] = O[cb][t] = zero4();
-#pragma unroll
-        for (int p = 0; p < KP; ++p) {
+        unroll<0, KP>([&](auto PI) {
+            constexpr int p = decltype(PI)::value, k = p % 2;
+            if constexpr (p + 1 < KP) {
+                load_k(kf[1 - k], c, p + 1);
+                if constexpr (!C::NARROW) load_q(qf[1 - k], c, p + 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             f16x8 sh[CPW], sl[CPW];
 #pragma unroll
             for (int cb = 0; cb < CPW; ++cb) split8(S[cb][2 * p], S[cb][2 * p + 1], sh[cb], sl[cb]);
+            if constexpr (C::NARROW) lds_st(xw + C::X_S + p * C::FR, sh[0]);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const f16x8 kf = lds_ld<f16x8>(Kt + (16 * t + r) * C::K::RS + 64 * p + 16 * g);
-                const f16x8 qf = lds_ld<f16x8>(Qt + (16 * t + r) * C::K::RS + 64 * p + 16 * g);
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int cb = 0; cb < CPW; ++cb) {
-                    Y[cb][t] = mfma32h(kf, sh[cb], Y[cb][t]);
-                    Y[cb][t] = mfma32h(kf, sl[cb], Y[cb][t]);
-                    O[cb][t] = mfma32h(sh[cb], qf, O[cb][t]);
-                }
+                for (int cb = 0; cb < CPW; ++cb) Y[cb][t] = mfma32h(kf[k][t], sh[cb], Y[cb][t]);
+            if constexpr (!C::NARROW) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int cb = 0; cb < CPW; ++cb) O[cb][t] = mfma32h(sh[cb], qf[k][t], O[cb][t]);
             }
-        }
-        // X = kPre beta V - beta e^G Y, in place of Y
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const f32x4 vb = *reinterpret_cast<const f32x4*>(vec + C::V_B / 4 + 16 * t + 4 * g);
-            const f32x4 ve = *reinterpret_cast<const f32x4*>(vec + C::V_BE / 4 + 16 * t + 4 * g);
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int cb = 0; cb < CPW; ++cb) {
-                const f32x4 vv = to_f4(lds_tr(Vt + tr_v + 16 * t * C::V::RS + 32 * (CPW * wave + cb)));
-                Y[cb][t] = vb * vv - ve * Y[cb][t];
-            }
-        }
-        // U: the upper half's solve, its substitution into the lower half's rows, that solve
-        f32x4 U[CPW][4];
-        f16x8 uh[CPW][2];
-#pragma unroll
-        for (int cb = 0; cb < CPW; ++cb) {
-            f16x8 xh, xl, ul;
-            split8(Y[cb][0], Y[cb][1], xh, xl);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const f16x8 th = frag(C::M_T0 + t * C::FR), tl = frag(C::M_T0 + (2 + t) * C::FR);
-                f32x4 u = mfma32h(tl, xh, zero4());
-                u = mfma32h(th, xl, u);
-                U[cb][t] = mfma32h(th, xh, u);
-            }
-            split8(U[cb][0], U[cb][1], uh[cb][0], ul);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const f16x8 ah = frag(C::M_A + t * C::FR), al = frag(C::M_A + (2 + t) * C::FR);
-                Y[cb][2 + t] = mfma32h(ah, uh[cb][0], Y[cb][2 + t]);
-                Y[cb][2 + t] = mfma32h(ah, ul, Y[cb][2 + t]);
-                Y[cb][2 + t] = mfma32h(al, uh[cb][0], Y[cb][2 + t]);
-            }
-            split8(Y[cb][2], Y[cb][3], xh, xl);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const f16x8 th = frag(C::M_T1 + t * C::FR), tl = frag(C::M_T1 + (2 + t) * C::FR);
-                f32x4 u = mfma32h(tl, xh, zero4());
-                u = mfma32h(th, xl, u);
-                U[cb][2 + t] = mfma32h(th, xh, u);
-            }
-            uh[cb][1] = to_h8(U[cb][2], U[cb][3]);
-        }
+                for (int cb = 0; cb < CPW; ++cb) Y[cb][t] = mfma32h(kf[k][t], sl[cb], Y[cb][t]);
+        });
         lds_barrier();
-        // O^T = e^G (Q S)^T + (P U)^T: lane (r, g) holds token r, columns 4g .. 4g+3
+        // U: the upper half's solve, its substitution into the lower half's rows, that solve.
+        // Operands are read before the products they wait for; the upper half's part of the
+        // state's update fills the wait for the lower half's.
+        struct Half {
+            f16x8 h[2], l[2];
+        };
+        auto load_half = [&](int off) {
+            return Half{{frag(off), frag(off + C::FR)}, {frag(off + 2 * C::FR), frag(off + 3 * C::FR)}};
+        };
+        // X = kPre beta V - beta e^G Y of half s, in place of Y
+        struct ValueRows {
+            f32x4 b[2], e[2];
+            bf16x4 v[CPW][2];
+        };
+        auto load_values = [&](int s) {
+            ValueRows x;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const float eg = vec[C::V_EG / 4 + 16 * t + r];
-            const int row = kGC * c + 16 * t + r;
+            for (int t = 0; t < 2; ++t) {
+                x.b[t] = tokens(C::V_B, 32 * s + 16 * t);
+                x.e[t] = tokens(C::V_BE, 32 * s + 16 * t);
 #pragma unroll
-            for (int cb = 0; cb < CPW; ++cb) {
-                f32x4 o = eg * O[cb][t];
-                o = mfma32h(uh[cb][0], frag(C::M_P + t * C::FR), o);
-                if (t >= 2) o = mfma32h(uh[cb][1], frag(C::M_P + (2 + t) * C::FR), o);
-                if (row < len)
-                    *reinterpret_cast<bf16x4*>(po + (int64_t)row * os + 16 * cb) = to_bf4(oscale * o);
+                for (int cb = 0; cb < CPW; ++cb)
+                    x.v[cb][t] = lds_tr(Vt + tr_v + (32 * s + 16 * t) * C::V::RS + 32 * (CPW * wave + cb));
             }
-        }
-        // S <- e^{G_C} S + K^T (e^{G_C - G} U)
-        const float gc = vec[C::V_GC / 4];
-        f16x8 wh[CPW][2], wl[CPW][2];
+            return x;
+        };
+        auto right_side = [&](const ValueRows& x, int s) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const f32x4 e0 = *reinterpret_cast<const f32x4*>(vec + C::V_ER / 4 + 32 * s + 4 * g);
-            const f32x4 e1 = *reinterpret_cast<const f32x4*>(vec + C::V_ER / 4 + 32 * s + 16 + 4 * g);
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int cb = 0; cb < CPW; ++cb) split8(e0 * U[cb][2 * s], e1 * U[cb][2 * s + 1], wh[cb][s], wl[cb][s]);
-        }
+                for (int cb = 0; cb < CPW; ++cb)
+                    Y[cb][2 * s + t] = x.b[t] * to_f4(x.v[cb][t]) - x.e[t] * Y[cb][2 * s + t];
+        };
+        const ValueRows v0 = load_values(0);
+        const Half T0 = load_half(C::M_T0);
+        const float gc = lds_ld<float>(vec + C::V_GC);
+        __builtin_amdgcn_sched_barrier(0);
+        const Half A = load_half(C::M_A);
+        const ValueRows v1 = load_values(1);
+        right_side(v0, 0);
+        f32x4 U[CPW][4];
+        f16x8 uh[CPW][2], ul[CPW];
+        auto solve = [&](const Half& T, int s) {
+            f16x8 xh[CPW], xl[CPW];
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
+            for (int cb = 0; cb < CPW; ++cb) split8(Y[cb][2 * s], Y[cb][2 * s + 1], xh[cb], xl[cb]);
 #pragma unroll
-            for (int cb = 0; cb < CPW; ++cb) S[cb][b] *= gc;
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const unsigned char* at = Kt + tr_k + 32 * s * C::K::RS + 64 * (b >> 1) + 8 * (b & 1);
-                const f16x8 kt = cat8h(lds_trh(at), lds_trh(at + 16 * C::K::RS));
+                for (int cb = 0; cb < CPW; ++cb) U[cb][2 * s + t] = mfma32h(T.l[t], xh[cb], zero4());
 #pragma unroll
-                for (int cb = 0; cb < CPW; ++cb) {
-                    S[cb][b] = mfma32h(kt, wl[cb][s], S[cb][b]);
-                    S[cb][b] = mfma32h(kt, wh[cb][s], S[cb][b]);
-                }
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int cb = 0; cb < CPW; ++cb) U[cb][2 * s + t] = mfma32h(T.h[t], xl[cb], U[cb][2 * s + t]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int cb = 0; cb < CPW; ++cb) U[cb][2 * s + t] = mfma32h(T.h[t], xh[cb], U[cb][2 * s + t]);
+        };
+        // S += K_s^T (e^{G_C - G} U_s) over the tokens of half s, four tiles of S at a time, the
+        // next four's columns of K read meanwhile
+        typedef f16x8 Cols[4];
+        auto load_cols = [&](Cols& x, int s, int b0) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const unsigned char* at = Kt + tr_k + 32 * s * C::K::RS + 64 * ((b0 + b) >> 1) + 8 * (b & 1);
+                x[b] = cat8h(lds_trh(at), lds_trh(at + 16 * C::K::RS));
             }
+        };
+        Cols kt[2];
+        auto update = [&](f32x4 e0, f32x4 e1, auto SI) {
+            constexpr int s = decltype(SI)::value;
+            f16x8 wh[CPW], wl[CPW];
+#pragma unroll
+            for (int cb = 0; cb < CPW; ++cb) split8(e0 * U[cb][2 * s], e1 * U[cb][2 * s + 1], wh[cb], wl[cb]);
+            unroll<0, KB / 4>([&](auto GI) {
+                constexpr int n = decltype(GI)::value;
+                if constexpr (n + 1 < KB / 4) load_cols(kt[1 - n % 2], s, 4 * (n + 1));
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int cb = 0; cb < CPW; ++cb) S[cb][4 * n + b] = mfma32h(kt[n % 2][b], wh[cb], S[cb][4 * n + b]);
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int cb = 0; cb < CPW; ++cb) S[cb][4 * n + b] = mfma32h(kt[n % 2][b], wl[cb], S[cb][4 * n + b]);
+            });
+        };
+        solve(T0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        right_side(v1, 1);
+        load_cols(kt[0], 0, 0);
+        f32x4 e0 = tokens(C::V_ER, 0), e1 = tokens(C::V_ER, 16);
+#pragma unroll
+        for (int cb = 0; cb < CPW; ++cb)
+#pragma unroll
+            for (int b = 0; b < KB; ++b) S[cb][b] *= gc;
+        __builtin_amdgcn_sched_barrier(0);
+        const Half T1 = load_half(C::M_T1);
+#pragma unroll
+        for (int cb = 0; cb < CPW; ++cb) split8(U[cb][0], U[cb][1], uh[cb][0], ul[cb]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int cb = 0; cb < CPW; ++cb) Y[cb][2 + t] = mfma32h(A.h[t], uh[cb][0], Y[cb][2 + t]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int cb = 0; cb < CPW; ++cb) Y[cb][2 + t] = mfma32h(A.h[t], ul[cb], Y[cb][2 + t]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int cb = 0; cb < CPW; ++cb) Y[cb][2 + t] = mfma32h(A.l[t], uh[cb][0], Y[cb][2 + t]);
+        update(e0, e1, i0);
+        solve(T1, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        load_cols(kt[0], 1, 0);
+        e0 = tokens(C::V_ER, 32);
+        e1 = tokens(C::V_ER, 48);
+#pragma unroll
+        for (int cb = 0; cb < CPW; ++cb) uh[cb][1] = to_h8(U[cb][2], U[cb][3]);
+        if constexpr (C::NARROW) {
+            lds_st(xw + C::X_U, uh[0][0]);
+            lds_st(xw + C::X_U + C::FR, uh[0][1]);
+        } else {
+            unroll<0, 4>([&](auto T) {
+                constexpr int t = decltype(T)::value;
+                const float eg = lds_ld<float>(vec + C::V_EG + 4 * (16 * t + r));
+#pragma unroll
+                for (int cb = 0; cb < CPW; ++cb) finish(eg * O[cb][t], uh[cb][0], uh[cb][1], T, c, 16 * (CPW * wave + cb));
+            });
+        }
+        update(e0, e1, i1);
+        __builtin_amdgcn_sched_barrier(0);
+        if (c + 1 < nch) {
+            load_k(kf[0], c + 1, 0);
+            if constexpr (!C::NARROW) load_q(qf[0], c + 1, 0);
         }
         lds_barrier();
     }
