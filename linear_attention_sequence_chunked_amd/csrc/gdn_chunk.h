@@ -99,19 +99,33 @@ __device__ __forceinline__ double wave_scan_f64(double x) {
 // it keep their accuracy and -inf - -inf does not arise; NaN stays.
 __device__ __forceinline__ double log2_decay(float la) { return (la < -1000.f ? -1000.0 : (double)la) * 1.4426950408889634074; }
 
+// x[i] += na[i] of lane J of the row of 16 times xj, four rows at once.  The compiler keeps the
+// broadcast and the FMA apart (twice the instructions of what bounds the inverse); the two wait
+// states cover a DPP read of a register that a VALU instruction has just written.
 template <int J>
-__device__ __forceinline__ float row_bcast(float x) { return dpp<0x150 + J>(x); }  // lane J of the row of 16
+__device__ __forceinline__ void fma_bcast4(float& x0, float& x1, float& x2, float& x3, float a0, float a1, float a2, float a3,
+                                           float xj) {
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %5, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %6, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %7, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+        : "+v"(x0), "+v"(x1), "+v"(x2), "+v"(x3)
+        : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "v"(xj), "n"(J));
+}
 
 // Inverse of the unit lower triangular 16x16 blocks I + A by forward substitution, one block per
-// 16 lanes: lane c holds A's column c (a[i] = A[i][c]) and gets the inverse's column c.  The
-// element a step needs is in lane j of the row, where the FMA reads it in place (DPP).
-__device__ __forceinline__ void invert16(const float (&a)[16], int col, float (&x)[16]) {
+// 16 lanes: lane c holds -A's column c (na[i] = -A[i][c], 0 for i <= c) and gets the inverse's
+// column c.  Rows are taken in whole groups of four: above the step's row they add 0.
+__device__ __forceinline__ void invert16(const float (&na)[16], int col, float (&x)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.f : 0.f;
     unroll<0, 15>([&](auto J) {
         constexpr int j = decltype(J)::value;
+        const float xj = x[j];
 #pragma unroll
-        for (int i = j + 1; i < 16; ++i) x[i] = fmaf(-row_bcast<j>(a[i]), x[j], x[i]);
+        for (int i = (j + 1) / 4 * 4; i < 16; i += 4)
+            fma_bcast4<j>(x[i], x[i + 1], x[i + 2], x[i + 3], na[i], na[i + 1], na[i + 2], na[i + 3], xj);
     });
 }
 
@@ -187,22 +201,22 @@ __device__ __forceinline__ f32x4 half_columns(const unsigned char* Kt, const uns
     const f32x4 es = decay_row(gv, t0 + 16 + r, t0 + 4 * g);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // selected, not multiplied: D above the diagonal may be inf
-        da[i] = 4 * g + i > r ? ba[i] * (ea[i] * da[i]) : 0.f;
-        db[i] = 4 * g + i > r ? bb[i] * (eb[i] * db[i]) : 0.f;
+        da[i] = 4 * g + i > r ? -ba[i] * (ea[i] * da[i]) : 0.f;
+        db[i] = 4 * g + i > r ? -bb[i] * (eb[i] * db[i]) : 0.f;
         sub[i] = bs * (es[i] * sub[i]);
     }
     lds_st(sc + I::COL * r + 16 * g, da);
     lds_st(sc + I::BLK + I::COL * r + 16 * g, db);
     wave_lds_sync();
-    float a[16], x[16];
+    float na[16], x[16];
     unsigned char* mine = sc + (g & 1) * I::BLK + I::COL * r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const f32x4 v = lds_ld<f32x4>(mine + 16 * i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a[4 * i + j] = v[j];
+        for (int j = 0; j < 4; ++j) na[4 * i + j] = v[j];
     }
-    invert16(a, r, x);
+    invert16(na, r, x);
     if (lane < 32) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) lds_st(mine + 16 * i, f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});

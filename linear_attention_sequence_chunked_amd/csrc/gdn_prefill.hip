@@ -82,22 +82,20 @@ struct PArgs {
     GdnTable tab;
 };
 
-__device__ __forceinline__ void split8(f32x4 a, f32x4 b, f16x8& hi, f16x8& lo) {
-    hi = to_h8(a, b);
-    f32x4 ra, rb;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        ra[i] = a[i] - (float)hi[i];
-        rb[i] = b[i] - (float)hi[4 + i];
-    }
-    lo = to_h8(ra, rb);
-}
-__device__ __forceinline__ void split4h(f32x4 a, f16x4& hi, f16x4& lo) {
+// x = hi + lo in fp16, 22 bits.  `m1` is -1 where the compiler cannot see it: fma(hi, m1, x)
+// rounded to fp16 is then one v_fma_mixlo/hi_f16 per element, against a conversion, a
+// subtraction and half a conversion if it is written as x - hi.
+__device__ __forceinline__ void split4h(f32x4 a, f16x4& hi, f16x4& lo, float m1) {
     hi = to_h4(a);
-    f32x4 ra;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ra[i] = a[i] - (float)hi[i];
-    lo = to_h4(ra);
+    for (int i = 0; i < 4; ++i) lo[i] = (_Float16)__builtin_fmaf((float)hi[i], m1, a[i]);
+}
+__device__ __forceinline__ void split8(f32x4 a, f32x4 b, f16x8& hi, f16x8& lo, float m1) {
+    f16x4 h0, h1, l0, l1;
+    split4h(a, h0, l0, m1);
+    split4h(b, h1, l1, m1);
+    hi = cat8h(h0, h1);
+    lo = cat8h(l0, l1);
 }
 
 template <int DK, int NCB>
@@ -126,9 +124,11 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
 
     constexpr int KB = C::KB, KP = C::KP, CPW = C::CPW;
     const float oscale = a.scale / kPre;
-    const int64_t os = (int64_t)a.hv * a.dv;
-    bf16* po = a.out + start * os + (int64_t)h * a.dv + col0 + 4 * g;
+    float m1 = -1.f;
+    asm("" : "+s"(m1));
+    const int os = a.hv * a.dv;  // output stride (the host bounds 64 rows of it to 32 bits)
 
+    using std::integral_constant;
     // ------------------------------------------------------------------ parts of the key side
     struct Staged {
         u32x4 k[C::K::PPT], q[C::K::PPT], v[C::V::PPT];
@@ -147,10 +147,10 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
             x.be = a.be[(at + lane) * a.hv + h];
         }
     };
-    auto stage = [&](const Staged& x, int c) {
+    auto stage = [&](const Staged& x, int c, auto CONVERT) {  // CONVERT: the rows are bf16 still
         unsigned char* Vt = buf(C::O_V, C::V::SIZE, c);
-        store_key<DK, true>(buf(C::O_K, C::K::SIZE, c), x.k, st);
-        store_key<DK, true>(buf(C::O_Q, C::K::SIZE, c), x.q, st);
+        store_key<DK, decltype(CONVERT)::value>(buf(C::O_K, C::K::SIZE, c), x.k, st);
+        store_key<DK, decltype(CONVERT)::value>(buf(C::O_Q, C::K::SIZE, c), x.q, st);
 #pragma unroll
         for (int i = 0; i < C::V::PPT; ++i) {
             const int e = st + 256 * i;
@@ -183,7 +183,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             f16x4 hi, lo;
-            split4h(rows[i], hi, lo);
+            split4h(rows[i], hi, lo, m1);
             lds_st(d + at[i], hi);
             lds_st(d + at[i] + 2 * C::FR, lo);
         }
@@ -212,14 +212,13 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
                 const f32x4 x = tile_dot<DK>(kj, ki);
                 const float nb = -lds_ld<float>(gv + GateVec::BE + 4 * (16 * it + r));
                 f16x4 hi, lo;
-                split4h(nb * (d * x), hi, lo);
+                split4h(nb * (d * x), hi, lo, m1);
                 unsigned char* m = M + C::M_A + (it % 2) * C::FR + 16 * lane + 8 * (jt % 2);
                 lds_st(m, hi);
                 lds_st(m + 2 * C::FR, lo);
             }
         });
     };
-    using std::integral_constant;
     constexpr integral_constant<int, 0> i0;
     constexpr integral_constant<int, 1> i1;
     constexpr integral_constant<int, 2> i2;
@@ -242,7 +241,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         if (nch > 0) load(x, 0);
         for (int c = 0; c <= nch; ++c) {
             if (c < nch) {
-                stage(x, c);
+                stage(x, c, integral_constant<bool, true>{});
                 if (c + 1 < nch) load(x, c + 1);
             }
             lds_barrier();
@@ -259,13 +258,29 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         return;
     }
     if (C::NARROW && wave >= C::W_STAGE && wave < C::W_INV) {
-        Staged x;
-        if (nch > 0) load(x, 0);
-        for (int c = 0; c <= nch; ++c) {
-            if (c < nch) stage(x, c);
-            if (c + 1 < nch) load(x, c + 1);
-            lds_barrier();
-            lds_barrier();
+        // two chunks of loads in flight; rows are converted in phase B, so that phase A only
+        // writes them
+        Staged x[2];
+        auto convert = [&](Staged& y) {
+#pragma unroll
+            for (int i = 0; i < C::K::PPT; ++i) {
+                y.k[i] = staged8<true>(y.k[i]);
+                y.q[i] = staged8<true>(y.q[i]);
+            }
+        };
+        if (nch > 0) load(x[0], 0);
+        if (nch > 1) load(x[1], 1);
+        convert(x[0]);
+        for (int c = 0; c <= nch; c += 2) {
+            unroll<0, 2>([&](auto J) {
+                constexpr int j = decltype(J)::value;
+                if (c + j > nch) return;
+                if (c + j < nch) stage(x[j], c + j, integral_constant<bool, false>{});
+                if (c + j + 2 < nch) load(x[j], c + j + 2);
+                lds_barrier();
+                if (c + j + 1 < nch) convert(x[1 - j]);
+                lds_barrier();
+            });
         }
         return;
     }
@@ -295,8 +310,12 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         const unsigned char* P = buf(C::O_M, C::M_SIZE, c) + C::M_P + 16 * lane;
         o = mfma32h(u0, lds_ld<f16x8>(P + t * C::FR), o);
         if constexpr (t >= 2) o = mfma32h(u1, lds_ld<f16x8>(P + (2 + t) * C::FR), o);
-        const int row = kGC * c + 16 * t + r;
-        if (row < len) *reinterpret_cast<bf16x4*>(po + (int64_t)row * os + col) = to_bf4(oscale * o);
+        // rows behind the sequence's last lie outside the buffer's range: not written
+        const int rows = min(kGC, len - kGC * c);
+        const __amdgpu_buffer_rsrc_t rs = rsrc(a.out + (start + (int64_t)kGC * c) * os + (int64_t)h * a.dv + col0,
+                                               ((rows - 1) * os + C::NV) * 2);
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, to_bf4(oscale * o)), rs, 2 * (r * os + 4 * g) + 2 * col,
+                                              32 * t * os, 0);
     };
     if (C::NARROW && wave == C::W_OUT) {
         f32x4 O[NCB][4];
@@ -406,7 +425,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
             }
             f16x8 sh[CPW], sl[CPW];
 #pragma unroll
-            for (int cb = 0; cb < CPW; ++cb) split8(S[cb][2 * p], S[cb][2 * p + 1], sh[cb], sl[cb]);
+            for (int cb = 0; cb < CPW; ++cb) split8(S[cb][2 * p], S[cb][2 * p + 1], sh[cb], sl[cb], m1);
             if constexpr (C::NARROW) lds_st(xw + C::X_S + p * C::FR, sh[0]);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -469,7 +488,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         auto solve = [&](const Half& T, int s) {
             f16x8 xh[CPW], xl[CPW];
 #pragma unroll
-            for (int cb = 0; cb < CPW; ++cb) split8(Y[cb][2 * s], Y[cb][2 * s + 1], xh[cb], xl[cb]);
+            for (int cb = 0; cb < CPW; ++cb) split8(Y[cb][2 * s], Y[cb][2 * s + 1], xh[cb], xl[cb], m1);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -498,7 +517,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
             constexpr int s = decltype(SI)::value;
             f16x8 wh[CPW], wl[CPW];
 #pragma unroll
-            for (int cb = 0; cb < CPW; ++cb) split8(e0 * U[cb][2 * s], e1 * U[cb][2 * s + 1], wh[cb], wl[cb]);
+            for (int cb = 0; cb < CPW; ++cb) split8(e0 * U[cb][2 * s], e1 * U[cb][2 * s + 1], wh[cb], wl[cb], m1);
             unroll<0, KB / 4>([&](auto GI) {
                 constexpr int n = decltype(GI)::value;
                 if constexpr (n + 1 < KB / 4) load_cols(kt[1 - n % 2], s, 4 * (n + 1));
@@ -524,7 +543,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         __builtin_amdgcn_sched_barrier(0);
         const Half T1 = load_half(C::M_T1);
 #pragma unroll
-        for (int cb = 0; cb < CPW; ++cb) split8(U[cb][0], U[cb][1], uh[cb][0], ul[cb]);
+        for (int cb = 0; cb < CPW; ++cb) split8(U[cb][0], U[cb][1], uh[cb][0], ul[cb], m1);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
