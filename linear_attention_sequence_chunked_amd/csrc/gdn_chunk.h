@@ -116,11 +116,11 @@ __device__ __forceinline__ void fma_bcast4(float& x0, float& x1, float& x2, floa
 
 // Inverse of the unit lower triangular 16x16 blocks I + A by forward substitution, one block per
 // 16 lanes: lane c holds -A's column c (na[i] = -A[i][c], 0 for i <= c) and gets the inverse's
-// column c.  Rows are taken in whole groups of four: above the step's row they add 0.
-__device__ __forceinline__ void invert16(const float (&na)[16], int col, float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.f : 0.f;
-    unroll<0, 15>([&](auto J) {
+// column c (x starts as the identity's).  Rows are taken in whole groups of four: above the
+// step's row they add 0.
+template <int J0, int J1>
+__device__ __forceinline__ void invert16(const float (&na)[16], float (&x)[16]) {  // steps J0 .. J1-1 of 15
+    unroll<J0, J1>([&](auto J) {
         constexpr int j = decltype(J)::value;
         const float xj = x[j];
 #pragma unroll
@@ -183,11 +183,16 @@ __device__ __forceinline__ f32x4 tile_dot(const TileRows<DK>& x, const TileRows<
 }
 
 // The 32x32 inverse of one half (rows and columns 32 half .. +31 of A) by one wave, in two
-// steps that a barrier may separate.  First A's tiles and the inverses of its diagonal blocks,
-// column by column into the scratch; `sub` is the block below them, lane (r, g): row r,
+// steps that a barrier may separate.  First A's tiles and the substitution's beginning in its
+// diagonal blocks (one per 16 lanes); `sub` is the block below them, lane (r, g): row r,
 // columns 4g .. 4g+3.
+struct HalfState {
+    f32x4 sub;
+    float na[16], x[16];
+};
+constexpr int kHalfSteps = 6;  // of 15 in the first step: the phases it is split over come out even
 template <int DK>
-__device__ __forceinline__ f32x4 half_columns(const unsigned char* Kt, const unsigned char* gv, unsigned char* sc, int half, int lane) {
+__device__ __forceinline__ HalfState half_columns(const unsigned char* Kt, const unsigned char* gv, unsigned char* sc, int half, int lane) {
     typedef InvScratch I;
     const int r = lane & 15, g = lane >> 4, t0 = 32 * half;
     TileRows<DK> k0, k1;
@@ -208,27 +213,34 @@ __device__ __forceinline__ f32x4 half_columns(const unsigned char* Kt, const uns
     lds_st(sc + I::COL * r + 16 * g, da);
     lds_st(sc + I::BLK + I::COL * r + 16 * g, db);
     wave_lds_sync();
-    float na[16], x[16];
-    unsigned char* mine = sc + (g & 1) * I::BLK + I::COL * r;
+    HalfState h;
+    h.sub = sub;
+    const unsigned char* mine = sc + (g & 1) * I::BLK + I::COL * r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const f32x4 v = lds_ld<f32x4>(mine + 16 * i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) na[4 * i + j] = v[j];
+        for (int j = 0; j < 4; ++j) {
+            h.na[4 * i + j] = v[j];
+            h.x[4 * i + j] = 4 * i + j == r ? 1.f : 0.f;
+        }
     }
-    invert16(na, r, x);
-    if (lane < 32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lds_st(mine + 16 * i, f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
-    }
-    wave_lds_sync();
-    return sub;
+    invert16<0, kHalfSteps>(h.na, h.x);
+    return h;
 }
-// Then the join.  rows[0]: row tile 0, columns 0..15; rows[1], rows[2]: row tile 1, columns
+// Then the rest of it, the inverses' columns through the scratch, and the join.  rows[0]: row tile 0, columns 0..15; rows[1], rows[2]: row tile 1, columns
 // 0..15 and 16..31; lane (r, g) gets row r, columns 4g .. 4g+3.
-__device__ __forceinline__ void half_join(const unsigned char* sc, f32x4 sub, int lane, f32x4 (&rows)[3]) {
+__device__ __forceinline__ void half_join(unsigned char* sc, HalfState& h, int lane, f32x4 (&rows)[3]) {
     typedef InvScratch I;
     const int r = lane & 15, g = lane >> 4;
+    invert16<kHalfSteps, 15>(h.na, h.x);
+    unsigned char* mine = sc + (g & 1) * I::BLK + I::COL * r;
+    if (lane < 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            lds_st(mine + 16 * i, f32x4{h.x[4 * i], h.x[4 * i + 1], h.x[4 * i + 2], h.x[4 * i + 3]});
+    }
+    wave_lds_sync();
     f32x4 tb;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -236,7 +248,7 @@ __device__ __forceinline__ void half_join(const unsigned char* sc, f32x4 sub, in
         tb[i] = lds_ld<float>(sc + I::BLK + I::COL * (4 * g + i) + 4 * r);
     }
     // M = A_10 T_a, then the transpose of -T_b M (its accumulator is a row fragment)
-    const f32x4 m = Mma<float>::run(sub, lds_ld<f32x4>(sc + I::COL * r + 16 * g), zero4());
+    const f32x4 m = Mma<float>::run(h.sub, lds_ld<f32x4>(sc + I::COL * r + 16 * g), zero4());
     rows[1] = -Mma<float>::run(m, tb, zero4());
     rows[2] = tb;
 }

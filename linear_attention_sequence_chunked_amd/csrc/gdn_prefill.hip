@@ -17,7 +17,7 @@
 //              phase A                             phase B
 //   stage      K, Q, V, decays of chunk c          (loads of c+1 in flight)
 //   inverse    (I + A)'s halves: join of c-1       tiles and substitution of c
-//   gram       P of c-1, lower rows                P of c, upper rows; A below the halves
+//   gram       P of c-1 within the halves          A and P below the halves of c
 //   chain      K S of c-1                          X, U of c-1, the state behind it
 //   out        P U of c-2, its rows stored         Q S of c-1
 // K, Q, V, the decays and the matrices are double-buffered; S and U reach the out wave as the
@@ -175,9 +175,9 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
     auto columns = [&](int c) {
         return half_columns<DK>(buf(C::O_K, C::K::SIZE, c), buf(C::O_G, GateVec::SIZE, c), isc, wave - C::W_INV, lane);
     };
-    auto join = [&](f32x4 sub, int c) {
+    auto join = [&](HalfState& x, int c) {
         f32x4 rows[3];
-        half_join(isc, sub, lane, rows);
+        half_join(isc, x, lane, rows);
         unsigned char* d = buf(C::O_M, C::M_SIZE, c) + (wave == C::W_INV ? C::M_T0 : C::M_T1) + 16 * lane;
         const int at[3] = {0, C::FR, C::FR + 8};
 #pragma unroll
@@ -188,17 +188,17 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
             lds_st(d + at[i] + 2 * C::FR, lo);
         }
     };
-    // P's tiles of row tile it from column tile J0 on, and -A's where they lie below the halves:
-    // lane (r, g) holds row 16 it + r, columns 16 jt + 4g ..
-    auto gram_row = [&](auto IT, auto J0, int c) {
+    // P's tiles (it, J0 .. J1-1), and -A's where they lie below the halves: lane (r, g) holds
+    // row 16 it + r, columns 16 jt + 4g ..
+    auto gram_row = [&](auto IT, auto J0, auto J1, int c) {
         constexpr int it = decltype(IT)::value;
         const unsigned char* Kt = buf(C::O_K, C::K::SIZE, c);
         const unsigned char* gv = buf(C::O_G, GateVec::SIZE, c);
         unsigned char* M = buf(C::O_M, C::M_SIZE, c);
         TileRows<DK> qt, ki;
         qt.load(buf(C::O_Q, C::K::SIZE, c), it, r, g);
-        if constexpr (it >= 2) ki.load(Kt, it, r, g);
-        unroll<decltype(J0)::value, it + 1>([&](auto JT) {
+        if constexpr (it >= 2 && decltype(J0)::value < 2) ki.load(Kt, it, r, g);
+        unroll<decltype(J0)::value, decltype(J1)::value>([&](auto JT) {
             constexpr int jt = decltype(JT)::value;
             TileRows<DK> kj;
             kj.load(Kt, jt, r, g);
@@ -223,15 +223,20 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
     constexpr integral_constant<int, 1> i1;
     constexpr integral_constant<int, 2> i2;
     constexpr integral_constant<int, 3> i3;
-    // one chunk's Gram work of gram wave n, first and second part
+    constexpr integral_constant<int, 4> i4;
+    // one chunk's Gram work of gram wave n: the block of A below the halves with P's tiles
+    // there, then P's other tiles (needed a phase later)
     auto gram_first = [&](int n, int c) {
-        if (n == 0) gram_row(i2, i0, c);
-        else gram_row(i3, i0, c);
+        if (n == 0) gram_row(i2, i0, i2, c);
+        else gram_row(i3, i0, i2, c);
     };
     auto gram_second = [&](int n, int c) {
         if (n == 0) {
-            gram_row(i1, i0, c);
-            gram_row(i0, i0, c);
+            gram_row(i2, i2, i3, c);
+            gram_row(i1, i0, i2, c);
+        } else {
+            gram_row(i3, i2, i4, c);
+            gram_row(i0, i0, i1, c);
         }
     };
 
@@ -247,7 +252,8 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
             lds_barrier();
             if (c < nch) {
                 if (wave < C::W_GRAM) {
-                    join(columns(c), c);
+                    HalfState x = columns(c);
+                    join(x, c);
                 } else {
                     gram_first(wave - C::W_GRAM, c);
                     gram_second(wave - C::W_GRAM, c);
@@ -285,11 +291,11 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         return;
     }
     if (C::NARROW && wave >= C::W_INV && wave < C::W_GRAM) {
-        f32x4 sub = zero4();
+        HalfState x = {};
         for (int c = 0; c <= nch; ++c) {
-            if (c > 0) join(sub, c - 1);
+            if (c > 0) join(x, c - 1);
             lds_barrier();
-            if (c < nch) sub = columns(c);
+            if (c < nch) x = columns(c);
             lds_barrier();
         }
         return;
@@ -442,6 +448,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
 #pragma unroll
                 for (int cb = 0; cb < CPW; ++cb) Y[cb][t] = mfma32h(kf[k][t], sl[cb], Y[cb][t]);
         });
+        __builtin_amdgcn_sched_barrier(0);  // the products stay in this phase
         lds_barrier();
         // U: the upper half's solve, its substitution into the lower half's rows, that solve.
         // Operands are read before the products they wait for; the upper half's part of the
