@@ -410,6 +410,38 @@ kda_status kda_gdn_chunk_prefill(const kda_gdn_params* params, const void* q, co
                                  void* stream);
 
 /*
+ * kda_gdn_prefill_backward -- gradients of kda_gdn_chunk_prefill (the training form).
+ *
+ * Given the forward's inputs and the gradients of its outputs, writes the gradient of the loss
+ * with respect to every input.  The loss is the one whose gradients are d_out (of out) and
+ * d_final_state (of final_state; NULL = zero).
+ *
+ *   q, k, v, log_alpha, beta, cu_seqlens_host, num_seqs, initial_state: the forward's
+ *   d_out           : [T_total, num_v_heads, dv], params->dtype, dense
+ *   d_final_state   : fp32 [num_seqs, num_v_heads, dk, dv] or NULL
+ *   dq, dk          : [T_total, num_k_heads, dk], params->dtype, dense: the sums over the value
+ *                     heads that share a key head, in fp32 and in head order, rounded once
+ *   dv              : [T_total, num_v_heads, dv], params->dtype, dense
+ *   dlog_alpha, dbeta : fp32 [T_total, num_v_heads]
+ *   d_initial_state : fp32 [num_seqs, num_v_heads, dk, dv] or NULL (not written)
+ *   workspace       : kda_gdn_prefill_backward_workspace bytes, 256-byte aligned; contents on
+ *                     entry do not matter.  Calls that share one must be ordered on one stream.
+ * No output and not the workspace may overlap another argument.  Results do not depend on the
+ * order in which the GPU runs the work: the same inputs give the same bits.
+ */
+kda_status kda_gdn_prefill_backward(const kda_gdn_params* params, const void* q, const void* k,
+                                    const void* v, const float* log_alpha, const float* beta,
+                                    const int32_t* cu_seqlens_host, int32_t num_seqs,
+                                    const float* initial_state, const void* d_out,
+                                    const float* d_final_state, void* dq, void* dk, void* dv,
+                                    float* dlog_alpha, float* dbeta, float* d_initial_state,
+                                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace kda_gdn_prefill_backward needs, or -1 if the arguments are invalid. */
+int64_t kda_gdn_prefill_backward_workspace(const kda_gdn_params* params,
+                                           const int32_t* cu_seqlens_host, int32_t num_seqs);
+
+/*
  * kda_gdn_recurrent -- num_tokens = K tokens (1 <= K <= 16) of every sequence from its stored
  * state, token by token: decoding (K = 1), the outputs of drafts (update_state = 0) and the
  * commit of their kept prefix (steps, out = NULL).

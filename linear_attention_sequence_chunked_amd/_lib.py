@@ -14,7 +14,8 @@ EXPORTED = ("kda_chunk_prefill", "kda_chunk_prefill_checkpointed", "kda_decode_s
             "kda_prefill_segmented_workspace", "kda_chunk_prefill_segmented_noalloc",
             "kda_noalloc_scratch_bytes", "kda_prefill_segment_plan", "kda_prefill_backward",
             "kda_prefill_backward_workspace", "kda_spec_accept", "kda_spec_accept_workspace",
-            "kda_gdn_chunk_prefill", "kda_gdn_recurrent", "kda_status_string", "kda_last_error",
+            "kda_gdn_chunk_prefill", "kda_gdn_recurrent", "kda_gdn_prefill_backward",
+            "kda_gdn_prefill_backward_workspace", "kda_status_string", "kda_last_error",
             "kda_abi_version")
 
 
@@ -95,6 +96,11 @@ def load() -> ctypes.CDLL:
     lib.kda_gdn_chunk_prefill.restype = ctypes.c_int
     lib.kda_gdn_recurrent.argtypes = [G, P, P, P, P, P, I32, I32, P, P, I32, P, I32, P, P]
     lib.kda_gdn_recurrent.restype = ctypes.c_int
+    lib.kda_gdn_prefill_backward.argtypes = [G, P, P, P, P, P, ctypes.POINTER(I32), I32, P, P, P, P,
+                                             P, P, P, P, P, P, I64, P]
+    lib.kda_gdn_prefill_backward.restype = ctypes.c_int
+    lib.kda_gdn_prefill_backward_workspace.argtypes = [G, ctypes.POINTER(I32), I32]
+    lib.kda_gdn_prefill_backward_workspace.restype = I64
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_last_error.argtypes = []

@@ -125,9 +125,111 @@ int32_t fill_table(kda::GdnTable& t, const int32_t* cu, const std::vector<int32_
     return n;
 }
 
+uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
+
+// Workspace of the backward: parts of dq and dk (shared key heads only), then what the form
+// needs.  Token by token: at most T/16 + num_seqs states per value head, and 16 states for each
+// workgroup that runs at once.
+struct BwdPlan {
+    uint64_t parts = 0, off_k = 0, off_a = 0, off_b = 0, total = 0;
+    int slots = 0;
+};
+BwdPlan plan_backward(const kda::GdnDims& d, const int32_t* cu, int32_t n) {
+    BwdPlan p;
+    const uint64_t T = (uint64_t)cu[n], hv = (uint64_t)d.hv, state = 4ull * d.dk * d.dv;
+    if (d.hv != d.hk) p.parts = align256(T * hv * d.dk * 4);
+    p.off_k = p.parts;
+    p.off_a = 2 * p.parts;
+    p.slots = (int)std::min<int64_t>((int64_t)std::min(n, kda::kGdnSeqs) * d.hv, 2 * kda::device_cu_count());
+    p.off_b = p.off_a + align256((T / 16 + n) * hv * state);
+    p.total = p.off_b + (uint64_t)p.slots * 16 * state;
+    return p;
+}
+
 }  // namespace
 
 extern "C" {
+
+int64_t kda_gdn_prefill_backward_workspace(const kda_gdn_params* params, const int32_t* cu_seqlens_host,
+                                           int32_t num_seqs) {
+    kda::GdnDims d;
+    if (check_gdn(params, d) != KDA_OK || check_cu(cu_seqlens_host, num_seqs) != KDA_OK) return -1;
+    kda::ok();
+    return (int64_t)plan_backward(d, cu_seqlens_host, num_seqs).total;
+}
+
+kda_status kda_gdn_prefill_backward(const kda_gdn_params* params, const void* q, const void* k,
+                                    const void* v, const float* log_alpha, const float* beta,
+                                    const int32_t* cu_seqlens_host, int32_t num_seqs,
+                                    const float* initial_state, const void* d_out,
+                                    const float* d_final_state, void* dq, void* dk, void* dv,
+                                    float* dlog_alpha, float* dbeta, float* d_initial_state,
+                                    void* workspace, int64_t workspace_bytes, void* stream) {
+    return guarded("kda_gdn_prefill_backward", [&]() -> kda_status {
+        kda::GdnBackwardArgs a = {};
+        kda_status st = check_gdn(params, a.d);
+        if (st != KDA_OK) return st;
+        if ((st = check_cu(cu_seqlens_host, num_seqs)) != KDA_OK) return st;
+        const kda::GdnDims& d = a.d;
+        const int64_t T = cu_seqlens_host[num_seqs];
+        const size_t es = element(d);
+        Range tok[5];
+        if ((st = check_tokens(d, T, q, k, v, log_alpha, beta, tok)) != KDA_OK) return st;
+        if (T > 0) {
+            const void* p[] = {d_out, dq, dk, dv};
+            const char* names[] = {"d_out", "dq", "dk", "dv"};
+            for (int i = 0; i < 4; ++i)
+                if ((st = check_ptr(names[i], p[i], 16)) != KDA_OK) return st;
+            if ((st = check_ptr("dlog_alpha", dlog_alpha, 4)) != KDA_OK) return st;
+            if ((st = check_ptr("dbeta", dbeta, 4)) != KDA_OK) return st;
+        }
+        if (initial_state && (st = check_ptr("initial_state", initial_state, 16)) != KDA_OK) return st;
+        if (d_final_state && (st = check_ptr("d_final_state", d_final_state, 16)) != KDA_OK) return st;
+        if (d_initial_state && (st = check_ptr("d_initial_state", d_initial_state, 16)) != KDA_OK) return st;
+        if ((st = check_ptr("workspace", workspace, 256)) != KDA_OK) return st;
+        const BwdPlan plan = plan_backward(d, cu_seqlens_host, num_seqs);
+        if (workspace_bytes < (int64_t)plan.total)
+            return fail(KDA_ERR_INVALID_ARGUMENT, "workspace_bytes %lld < %llu needed", (long long)workspace_bytes,
+                        (unsigned long long)plan.total);
+        const uint64_t nk = (uint64_t)T * d.hk * d.dk * es, nv = (uint64_t)T * d.hv * d.dv * es, ng = (uint64_t)T * d.hv * 4;
+        const uint64_t ns = (uint64_t)num_seqs * d.hv * d.dk * d.dv * 4;
+        const Range ins[] = {tok[0], tok[1], tok[2], tok[3], tok[4], range("d_out", d_out, nv),
+                             range("initial_state", initial_state, ns), range("d_final_state", d_final_state, ns)};
+        const Range outs[] = {range("dq", dq, nk), range("dk", dk, nk), range("dv", dv, nv),
+                              range("dlog_alpha", dlog_alpha, ng), range("dbeta", dbeta, ng),
+                              range("d_initial_state", d_initial_state, ns), range("workspace", workspace, plan.total)};
+        for (size_t i = 0; i < sizeof(outs) / sizeof(outs[0]); ++i) {
+            for (const Range& r : ins)
+                if (overlaps(outs[i], r)) return fail(KDA_ERR_INVALID_ARGUMENT, "%s overlaps %s", outs[i].name, r.name);
+            for (size_t j = 0; j < i; ++j)
+                if (overlaps(outs[i], outs[j]))
+                    return fail(KDA_ERR_INVALID_ARGUMENT, "%s overlaps %s", outs[i].name, outs[j].name);
+        }
+        if ((st = check_grid(std::min<int64_t>(num_seqs, kda::kGdnSeqs) * d.hv * (d.dv / 16))) != KDA_OK) return st;
+        if ((st = check_grid(T * d.hk * (d.dk / 4) / 256 + 1)) != KDA_OK) return st;
+        a.T = T; a.q = q; a.k = k; a.v = v; a.d_out = d_out; a.log_alpha = log_alpha; a.beta = beta;
+        a.initial_state = initial_state; a.d_final_state = d_final_state; a.dq = dq; a.dk = dk; a.dv = dv;
+        a.dlog_alpha = dlog_alpha; a.dbeta = dbeta; a.d_initial_state = d_initial_state;
+        char* ws = static_cast<char*>(workspace);
+        a.parts = plan.parts > 0;
+        a.dq_parts = reinterpret_cast<float*>(ws);
+        a.dk_parts = reinterpret_cast<float*>(ws + plan.off_k);
+        a.checkpoints = reinterpret_cast<float*>(ws + plan.off_a);
+        a.scratch = reinterpret_cast<float*>(ws + plan.off_b);
+        a.slots = plan.slots;
+        const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+        const std::vector<int32_t> order = longest_first(cu_seqlens_host, num_seqs);
+        kda::GdnTable tab;
+        hipError_t e = hipSuccess;
+        for (int32_t from = 0; from < num_seqs && e == hipSuccess; from += a.num_seqs) {
+            a.num_seqs = fill_table(tab, cu_seqlens_host, order, from);
+            e = kda::launch_gdn_backward_seq(a, tab, hs);
+        }
+        if (e == hipSuccess && a.parts) e = kda::launch_gdn_sum_parts(a, hs);
+        if (e != hipSuccess) return fail(KDA_ERR_HIP, "kda_gdn_prefill_backward launch: %s", hipGetErrorString(e));
+        return kda::ok();
+    });
+}
 
 kda_status kda_gdn_chunk_prefill(const kda_gdn_params* params, const void* q, const void* k,
                                  const void* v, const float* log_alpha, const float* beta,

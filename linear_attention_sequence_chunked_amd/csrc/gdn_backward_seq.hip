@@ -1,0 +1,276 @@
+// gdn_backward_seq.hip -- gradients of the gated delta rule token by token (gfx950): the form
+// of 32-bit inputs.
+//
+// Per (sequence, value head), backwards over the tokens, D the gradient of the state behind
+// token t (A = e^{g} S the decayed state, err = v - A^T k, u = beta err, S' = A + k u^T):
+//   dq = scale S' do            D += scale q do^T           du = D^T k
+//   dk = D u - A (beta du)      dbeta = du . err            dv = beta du
+//   D -= k (beta du)^T          dg = <D, A>                 D <- e^{g} D
+// A walk forwards keeps the state before every 16th token; backwards, each block of 16 is run
+// again from there with its decayed states A written to a scratch (L2-resident: 1 MiB per
+// workgroup), so no state is ever divided by its decay.  Everything is fp32.
+//
+// One workgroup of four waves holds a whole state: thread t has columns 4 (t % COLG) .. +3 of
+// RPT consecutive rows.  Column sums (du) go through LDS, one barrier per token; row sums
+// (dq, dk) are reduced among the COLG threads of a row group, halving the rows at each step.
+// Bound by those reductions and the barrier (latency), not by memory.
+//
+// Heads that share a key head write their parts of dq and dk apart; a second launch adds them
+// in head order.
+#include <algorithm>
+
+#include "gdn_launch.h"
+#include "kda_device.h"
+#include "kda_launch.h"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int TB = 16;
+
+__device__ inline f32x4 load4f(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ inline f32x4 load4f(const bf16* p) { return __builtin_convertvector(*reinterpret_cast<const bf16x4*>(p), f32x4); }
+
+template <typename T, int DK, int DV>
+struct Shape {
+    static constexpr int COLG = DV / 4, ROWG = kThreads / COLG, RPT = DK / ROWG;
+    static constexpr int64_t STATE = (int64_t)DK * DV;
+};
+
+// sums over the COLG threads of a row group of RPT values each: thread c returns the sum of
+// value `row` (set for c < RPT's share, see use)
+template <int N, int LANES>
+__device__ inline float reduce_rows(float (&v)[N], int c, int& row) {
+    row = 0;
+    int off = 1;
+#pragma unroll
+    for (int n = N; n > 1; n /= 2) {
+        const bool up = c & off;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float keep = up ? v[i + n / 2] : v[i], give = up ? v[i] : v[i + n / 2];
+            v[i] = keep + __shfl_xor(give, off);
+        }
+        row += up ? n / 2 : 0;
+        off *= 2;
+    }
+#pragma unroll
+    for (; off < LANES; off *= 2) v[0] += __shfl_xor(v[0], off);
+    return v[0];
+}
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArgs A, const GdnTable tab, int pairs) {
+    using L = Shape<T, DK, DV>;
+    constexpr int COLG = L::COLG, RPT = L::RPT;
+    __shared__ __attribute__((aligned(16))) float s_k[TB][DK], s_q[TB][DK], s_v[TB][DV], s_do[TB][DV];
+    __shared__ float s_a[TB], s_b[TB], s_g[TB][4];
+    __shared__ f32x4 s_red[2][4][COLG];
+    const int t = threadIdx.x, cg = t % COLG, rg = t / COLG, wave = t / 64, lane = t % 64;
+    float* scratch = A.scratch + (int64_t)blockIdx.x * TB * L::STATE;
+    const int64_t at = (int64_t)(rg * RPT) * DV + 4 * cg;
+    const GdnDims& d = A.d;
+
+    for (int pair = blockIdx.x; pair < pairs; pair += gridDim.x) {
+        const int si = pair / d.hv, h = pair % d.hv, hk = h / (d.hv / d.hk), len = tab.len[si], id = tab.id[si];
+        const int64_t start = tab.start[si], ss = ((int64_t)id * d.hv + h) * L::STATE;
+        // the state before block b of this sequence and head
+        float* keep = A.checkpoints + ((start / TB + id) * d.hv + (int64_t)h * ((len + TB - 1) / TB)) * L::STATE;
+        const int blocks = (len + TB - 1) / TB;
+
+        auto stage = [&](int b) {
+            const int m = min(TB, len - TB * b);
+            const int64_t row0 = start + (int64_t)TB * b;
+            __syncthreads();
+            for (int e = t; e < TB * DK / 4; e += kThreads) {
+                const int r = e / (DK / 4), c = 4 * (e % (DK / 4));
+                f32x4 kv = zero4(), qv = zero4();
+                if (r < m) {
+                    kv = load4f((const T*)A.k + (row0 + r) * d.ks + (int64_t)hk * DK + c);
+                    qv = load4f((const T*)A.q + (row0 + r) * d.qs + (int64_t)hk * DK + c);
+                }
+                *reinterpret_cast<f32x4*>(&s_k[r][c]) = kv;
+                *reinterpret_cast<f32x4*>(&s_q[r][c]) = qv * d.scale;
+            }
+            for (int e = t; e < TB * DV / 4; e += kThreads) {
+                const int r = e / (DV / 4), c = 4 * (e % (DV / 4));
+                f32x4 vv = zero4(), ov = zero4();
+                if (r < m) {
+                    vv = load4f((const T*)A.v + (row0 + r) * d.vs + (int64_t)h * DV + c);
+                    ov = load4f((const T*)A.d_out + ((row0 + r) * d.hv + h) * (int64_t)DV + c);
+                }
+                *reinterpret_cast<f32x4*>(&s_v[r][c]) = vv;
+                *reinterpret_cast<f32x4*>(&s_do[r][c]) = ov;
+            }
+            if (t < m) {
+                s_a[t] = expf(A.log_alpha[(row0 + t) * d.hv + h]);
+                s_b[t] = A.beta[(row0 + t) * d.hv + h];
+            }
+            __syncthreads();
+            return m;
+        };
+        int turn = 0;
+        // sum over all rows of this thread's columns
+        auto column_sum = [&](f32x4 w) {
+#pragma unroll
+            for (int off = COLG; off < 64; off <<= 1)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) w[c] += __shfl_xor(w[c], off);
+            if (lane < COLG) s_red[turn][wave][lane] = w;
+            __syncthreads();
+            w = (s_red[turn][0][cg] + s_red[turn][1][cg]) + (s_red[turn][2][cg] + s_red[turn][3][cg]);
+            turn ^= 1;
+            return w;
+        };
+        f32x4 S[RPT];
+        // tokens 0 .. m-1 of the staged block; SAVE: their decayed states to the scratch, and
+        // err over v
+        auto forward = [&](int m, bool save) {
+            for (int j = 0; j < m; ++j) {
+                f32x4 w = zero4();
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) {
+                    S[i] *= s_a[j];
+                    w += S[i] * s_k[j][rg * RPT + i];
+                    if (save) *reinterpret_cast<f32x4*>(scratch + j * L::STATE + at + i * DV) = S[i];
+                }
+                w = column_sum(w);
+                const f32x4 err = *reinterpret_cast<const f32x4*>(&s_v[j][4 * cg]) - w;
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) S[i] += s_k[j][rg * RPT + i] * (s_b[j] * err);
+                if (save) {
+                    __syncthreads();  // every row group has read v
+                    if (rg == 0) *reinterpret_cast<f32x4*>(&s_v[j][4 * cg]) = err;
+                }
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) S[i] = A.initial_state ? *reinterpret_cast<const f32x4*>(A.initial_state + ss + at + i * DV) : zero4();
+        for (int b = 0; b < blocks; ++b) {
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) *reinterpret_cast<f32x4*>(keep + b * L::STATE + at + i * DV) = S[i];
+            if (b + 1 == blocks) break;
+            forward(stage(b), false);
+        }
+        f32x4 D[RPT];
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) D[i] = A.d_final_state ? *reinterpret_cast<const f32x4*>(A.d_final_state + ss + at + i * DV) : zero4();
+        for (int b = blocks - 1; b >= 0; --b) {
+            const int m = stage(b);
+            const int64_t row0 = start + (int64_t)TB * b;
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) S[i] = *reinterpret_cast<const f32x4*>(keep + b * L::STATE + at + i * DV);
+            forward(m, true);
+            __syncthreads();
+            for (int j = m - 1; j >= 0; --j) {
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) S[i] = *reinterpret_cast<const f32x4*>(scratch + j * L::STATE + at + i * DV);
+                const float a = s_a[j], be = s_b[j];
+                const f32x4 err = *reinterpret_cast<const f32x4*>(&s_v[j][4 * cg]), u = be * err;
+                const f32x4 go = *reinterpret_cast<const f32x4*>(&s_do[j][4 * cg]);
+                float pq[RPT], pk[RPT];
+                f32x4 w = zero4();
+                auto dot = [](f32x4 x, f32x4 y) { return (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]); };
+                const float udo = dot(u, go);
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) {
+                    const float kr = s_k[j][rg * RPT + i];
+                    pq[i] = dot(S[i], go) + kr * udo;  // of S' do
+                    D[i] += s_q[j][rg * RPT + i] * go;
+                    w += D[i] * kr;
+                }
+                const f32x4 du = column_sum(w), bdu = be * du;
+                float dg = 0.f;
+#pragma unroll
+                for (int i = 0; i < RPT; ++i) {
+                    pk[i] = dot(D[i], u) - dot(S[i], bdu);
+                    D[i] -= s_k[j][rg * RPT + i] * bdu;
+                    dg += dot(D[i], S[i]);
+                    D[i] *= a;
+                }
+                int row;
+                const float rq = reduce_rows<RPT, COLG>(pq, cg, row), rk = reduce_rows<RPT, COLG>(pk, cg, row);
+                if (cg < RPT) {
+                    const int64_t o = (A.parts ? ((row0 + j) * d.hv + h) : ((row0 + j) * d.hk + hk)) * (int64_t)DK + rg * RPT + row;
+                    if (A.parts) {
+                        A.dq_parts[o] = d.scale * rq;
+                        A.dk_parts[o] = rk;
+                    } else {
+                        ((T*)A.dq)[o] = from_f32<T>(d.scale * rq);
+                        ((T*)A.dk)[o] = from_f32<T>(rk);
+                    }
+                }
+                const float db = dot(du, err);
+                float sum = db;
+#pragma unroll
+                for (int off = 1; off < COLG; off <<= 1) sum += __shfl_xor(sum, off);
+                if (rg == 0) {
+                    store4((T*)A.dv + ((row0 + j) * d.hv + h) * (int64_t)DV + 4 * cg, Mma<T>::pack(bdu));
+                    if (cg == 0) A.dbeta[(row0 + j) * d.hv + h] = sum;
+                }
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1) dg += __shfl_xor(dg, off);
+                if (lane == 0) s_g[j][wave] = dg;
+            }
+            __syncthreads();
+            if (t < m) A.dlog_alpha[(row0 + t) * d.hv + h] = (s_g[t][0] + s_g[t][1]) + (s_g[t][2] + s_g[t][3]);
+        }
+        if (A.d_initial_state) {
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) *reinterpret_cast<f32x4*>(A.d_initial_state + ss + at + i * DV) = D[i];
+        }
+        __syncthreads();
+    }
+}
+
+// dq and dk of a key head: the sums over the value heads that share it, in head order
+template <typename T>
+__global__ __launch_bounds__(256) void sum_parts_kernel(const GdnBackwardArgs A, int64_t total4, int dk4) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total4) return;
+    const int group = A.d.hv / A.d.hk;
+    const int64_t c = i % dk4, th = i / dk4;  // th: token and key head
+    const int64_t src = th * group * dk4 + c;
+    f32x4 q = zero4(), k = zero4();
+    for (int n = 0; n < group; ++n) {
+        q += reinterpret_cast<const f32x4*>(A.dq_parts)[src + (int64_t)n * dk4];
+        k += reinterpret_cast<const f32x4*>(A.dk_parts)[src + (int64_t)n * dk4];
+    }
+    store4((T*)A.dq + 4 * i, Mma<T>::pack(q));
+    store4((T*)A.dk + 4 * i, Mma<T>::pack(k));
+}
+
+template <typename T>
+hipError_t sum_parts(const GdnBackwardArgs& a, hipStream_t st) {
+    const int64_t total4 = a.T * a.d.hk * (a.d.dk / 4);
+    if (total4 == 0) return hipSuccess;
+    hipLaunchKernelGGL((sum_parts_kernel<T>), dim3((unsigned)((total4 + 255) / 256)), dim3(256), 0, st, a, total4, a.d.dk / 4);
+    return hipGetLastError();
+}
+
+template <typename T, int DK, int DV>
+hipError_t launch(const GdnBackwardArgs& a, const GdnTable& tab, hipStream_t st) {
+    const int pairs = a.num_seqs * a.d.hv;
+    if (pairs == 0) return hipSuccess;
+    hipLaunchKernelGGL((backward_kernel<T, DK, DV>), dim3((unsigned)std::min(pairs, a.slots)), dim3(kThreads), 0, st, a, tab, pairs);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t dispatch(const GdnBackwardArgs& a, const GdnTable& tab, hipStream_t st) {
+    if (a.d.dk == 128) return a.d.dv == 128 ? launch<T, 128, 128>(a, tab, st) : launch<T, 128, 64>(a, tab, st);
+    return a.d.dv == 128 ? launch<T, 64, 128>(a, tab, st) : launch<T, 64, 64>(a, tab, st);
+}
+
+}  // namespace
+
+hipError_t launch_gdn_backward_seq(const GdnBackwardArgs& a, const GdnTable& tab, hipStream_t st) {
+    return a.d.dtype == DTYPE_BF16 ? dispatch<bf16>(a, tab, st) : dispatch<float>(a, tab, st);
+}
+
+hipError_t launch_gdn_sum_parts(const GdnBackwardArgs& a, hipStream_t st) {
+    return a.d.dtype == DTYPE_BF16 ? sum_parts<bf16>(a, st) : sum_parts<float>(a, st);
+}
+
+}  // namespace kda

@@ -50,6 +50,23 @@ struct GdnRecurrentArgs {
     int nv;
 };
 
+struct GdnBackwardArgs {
+    GdnDims d;
+    int num_seqs;
+    int64_t T;                    // packed tokens
+    const void *q, *k, *v, *d_out;
+    const float *log_alpha, *beta;
+    const float *initial_state, *d_final_state;  // may be null
+    void *dq, *dk, *dv;
+    float *dlog_alpha, *dbeta;
+    float* d_initial_state;       // may be null
+    bool parts;                   // shared key heads: dq and dk of each value head apart first
+    float *dq_parts, *dk_parts;   // [T, hv, dk]
+    // token by token: states before every 16th token, and a scratch of 16 states per workgroup
+    float *checkpoints, *scratch;
+    int slots;                    // workgroups the scratch serves
+};
+
 struct AcceptArgs {
     int dtype, num_seqs, num_draft;
     int64_t vocab;
@@ -73,6 +90,8 @@ int accept_pieces(int64_t num_seqs, int64_t vocab, int cu_count);
 hipError_t launch_gdn_recurrent(const GdnRecurrentArgs& a, hipStream_t stream);
 hipError_t launch_gdn_sequential(const GdnPrefillArgs& a, const GdnTable& t, hipStream_t stream);
 hipError_t launch_gdn_chunked(const GdnPrefillArgs& a, const GdnTable& t, hipStream_t stream);
+hipError_t launch_gdn_backward_seq(const GdnBackwardArgs& a, const GdnTable& t, hipStream_t stream);
+hipError_t launch_gdn_sum_parts(const GdnBackwardArgs& a, hipStream_t stream);
 hipError_t launch_accept(const AcceptArgs& a, hipStream_t stream);
 
 }  // namespace kda

@@ -130,6 +130,47 @@ def gdn_chunk_prefill(q, k, v, log_alpha, beta, cu_seqlens: Optional[Sequence[in
     return out, final_state
 
 
+def gdn_prefill_backward(q, k, v, log_alpha, beta, d_out,
+                         cu_seqlens: Optional[Sequence[int]] = None, initial_state=None,
+                         d_final_state=None, scale: float = 1.0,
+                         workspace: Optional[torch.Tensor] = None):
+    """Gradients of gdn_chunk_prefill.  Inputs as for gdn_chunk_prefill, d_out like o (dense),
+    d_final_state fp32 [N, HV, dk, dv] or None.  Returns a dict with dq, dk, dv (dtypes and
+    shapes of q, k, v), dlog_alpha and dbeta (fp32) and d_initial_state (fp32 [N, HV, dk, dv]).
+    workspace: a uint8 tensor of at least kda_gdn_prefill_backward_workspace bytes, or None to
+    allocate one."""
+    cu, T = _lengths(q, cu_seqlens)
+    N, dev = len(cu) - 1, q.device
+    p = _params(q, k, v, tuple(q.shape[:-2]), scale)
+    hv, dk, dv = p.num_v_heads, p.dk, p.dv
+    gshape = tuple(q.shape[:-2]) + (hv,)
+    _gates("log_alpha", log_alpha, gshape, dev)
+    _gates("beta", beta, gshape, dev)
+    _check_out("d_out", d_out, v.shape, v.dtype, dev)
+    for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state)):
+        if t is not None:
+            _check_out(name, t, (N, hv, dk, dv), torch.float32, dev)
+    new = lambda like, dtype: torch.empty(like.shape, dtype=dtype, device=dev)  # noqa: E731
+    g = dict(dq=new(q, q.dtype), dk=new(k, k.dtype), dv=new(v, v.dtype), dlog_alpha=new(log_alpha, torch.float32),
+             dbeta=new(beta, torch.float32),
+             d_initial_state=torch.empty((N, hv, dk, dv), dtype=torch.float32, device=dev))
+    lib, cu_h = _lib.load(), (ctypes.c_int32 * (N + 1))(*cu)
+    with _on(dev) as stream:
+        if workspace is None:
+            need = lib.kda_gdn_prefill_backward_workspace(ctypes.byref(p), cu_h, N)
+            if need < 0:
+                raise _lib.KdaError(_lib.KDA_ERR_INVALID_ARGUMENT, lib.kda_last_error().decode())
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        else:
+            _check_out("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+        _lib.check(lib.kda_gdn_prefill_backward(
+            ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), cu_h, N,
+            _ptr(initial_state), _ptr(d_out), _ptr(d_final_state), _ptr(g["dq"]), _ptr(g["dk"]),
+            _ptr(g["dv"]), _ptr(g["dlog_alpha"]), _ptr(g["dbeta"]), _ptr(g["d_initial_state"]),
+            _ptr(workspace), workspace.numel(), stream))
+    return g
+
+
 def gdn_recurrent(q, k, v, log_alpha, beta, state, steps: Optional[torch.Tensor] = None,
                   state_indices: Optional[torch.Tensor] = None, update_state: bool = True,
                   output: bool = True, scale: float = 1.0, out: Optional[torch.Tensor] = None):

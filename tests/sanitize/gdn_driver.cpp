@@ -23,6 +23,11 @@ hipError_t launch_gdn_chunked(const GdnPrefillArgs& a, const GdnTable& t, hipStr
     return a.d.dv % a.nv ? hipErrorInvalidValue : launch_gdn_sequential(a, t, s);
 }
 hipError_t launch_gdn_recurrent(const GdnRecurrentArgs&, hipStream_t) { return hipErrorNotSupported; }
+hipError_t launch_gdn_backward_seq(const GdnBackwardArgs& a, const GdnTable& t, hipStream_t) {
+    for (int i = 0; i < a.num_seqs; ++i) g_tokens += t.len[i];
+    return a.slots > 0 ? hipSuccess : hipErrorInvalidValue;
+}
+hipError_t launch_gdn_sum_parts(const GdnBackwardArgs& a, hipStream_t) { return a.parts ? hipSuccess : hipErrorInvalidValue; }
 hipError_t launch_accept(const AcceptArgs& a, hipStream_t) {
     return a.piece * a.pieces >= a.vocab && a.pieces <= 256 ? hipErrorNotSupported : hipSuccess;
 }
@@ -52,6 +57,19 @@ int main() {
             g_longest = 1 << 30;
             expect(kda_gdn_chunk_prefill(&p, at(1), at(2), at(3), fl(4), fl(5), cu.data(), n, fl(6), fl(6), at(7), nullptr),
                    KDA_OK, "prefill");
+        }
+        for (int dt : {KDA_DTYPE_BF16, KDA_DTYPE_F32}) {
+            p.dtype = dt;
+            const long long ws = kda_gdn_prefill_backward_workspace(&p, cu.data(), n);
+            const long long before = g_tokens;
+            expect(kda_gdn_prefill_backward(&p, at(1), at(2), at(3), fl(4), fl(5), cu.data(), n, nullptr, at(8), nullptr, at(9),
+                                            at(10), at(11), fl(12), fl(13), nullptr, (void*)(1ull << 50), ws, nullptr),
+                   KDA_OK, "backward");
+            expect(g_tokens - before == cu[n], 1, "every token once");
+            g_tokens = before;
+            expect(kda_gdn_prefill_backward(&p, at(1), at(2), at(3), fl(4), fl(5), cu.data(), n, nullptr, at(8), nullptr, at(9),
+                                            at(10), at(11), fl(12), fl(13), nullptr, (void*)(1ull << 50), ws - 1, nullptr),
+                   KDA_ERR_INVALID_ARGUMENT, "a byte short");
         }
         expect(g_seqs == 2 * n && g_tokens == 2 * cu[n], 1, "every sequence once");
     }
