@@ -18,7 +18,7 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_plan.cpp", "kda_decode.hip", "kda_prefill.hip", "kda_prefill_bf16.hip",
            "kda_spec.hip", "kda_segment.hip", "kda_backward.hip", "kda_scratch.hip",
-           "gdn_api.cpp", "gdn_plan.cpp", "gdn_recurrent.hip", "gdn_prefill.hip", "gdn_backward_seq.hip",
+           "gdn_api.cpp", "gdn_plan.cpp", "gdn_recurrent.hip", "gdn_prefill.hip", "gdn_backward.hip", "gdn_backward_seq.hip",
            "spec_accept.hip"]
 HEADERS = ["kda_device.h", "kda_launch.h", "kda_mfma.h", "kda_check.h", "gdn_launch.h", "gdn_chunk.h"]
 

@@ -128,10 +128,12 @@ int32_t fill_table(kda::GdnTable& t, const int32_t* cu, const std::vector<int32_
 uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
 // Workspace of the backward: parts of dq and dk (shared key heads only), then what the form
-// needs.  Token by token: at most T/16 + num_seqs states per value head, and 16 states for each
+// needs.  In chunks (bf16): per chunk and value head the state before it, the gradient of the
+// state behind it, U and dX, four bytes an element; at most T/64 + num_seqs chunks per head.
+// Token by token: at most T/16 + num_seqs states per value head, and 16 states for each
 // workgroup that runs at once.
 struct BwdPlan {
-    uint64_t parts = 0, off_k = 0, off_a = 0, off_b = 0, total = 0;
+    uint64_t parts = 0, off_k = 0, off_a = 0, off_b = 0, off_c = 0, off_d = 0, total = 0;
     int slots = 0;
 };
 BwdPlan plan_backward(const kda::GdnDims& d, const int32_t* cu, int32_t n) {
@@ -140,6 +142,14 @@ BwdPlan plan_backward(const kda::GdnDims& d, const int32_t* cu, int32_t n) {
     if (d.hv != d.hk) p.parts = align256(T * hv * d.dk * 4);
     p.off_k = p.parts;
     p.off_a = 2 * p.parts;
+    if (d.dtype == KDA_DTYPE_BF16) {
+        const uint64_t chunks = (T / 64 + n) * hv, rows = 4ull * 64 * d.dv;
+        p.off_b = p.off_a + align256(chunks * state);
+        p.off_c = p.off_b + align256(chunks * state);
+        p.off_d = p.off_c + align256(chunks * rows);
+        p.total = p.off_d + align256(chunks * rows);
+        return p;
+    }
     p.slots = (int)std::min<int64_t>((int64_t)std::min(n, kda::kGdnSeqs) * d.hv, 2 * kda::device_cu_count());
     p.off_b = p.off_a + align256((T / 16 + n) * hv * state);
     p.total = p.off_b + (uint64_t)p.slots * 16 * state;
@@ -207,6 +217,7 @@ kda_status kda_gdn_prefill_backward(const kda_gdn_params* params, const void* q,
         }
         if ((st = check_grid(std::min<int64_t>(num_seqs, kda::kGdnSeqs) * d.hv * (d.dv / 16))) != KDA_OK) return st;
         if ((st = check_grid(T * d.hk * (d.dk / 4) / 256 + 1)) != KDA_OK) return st;
+        if ((st = check_grid((T / 64 + 1) * d.hv)) != KDA_OK) return st;
         a.T = T; a.q = q; a.k = k; a.v = v; a.d_out = d_out; a.log_alpha = log_alpha; a.beta = beta;
         a.initial_state = initial_state; a.d_final_state = d_final_state; a.dq = dq; a.dk = dk; a.dv = dv;
         a.dlog_alpha = dlog_alpha; a.dbeta = dbeta; a.d_initial_state = d_initial_state;
@@ -214,16 +225,22 @@ kda_status kda_gdn_prefill_backward(const kda_gdn_params* params, const void* q,
         a.parts = plan.parts > 0;
         a.dq_parts = reinterpret_cast<float*>(ws);
         a.dk_parts = reinterpret_cast<float*>(ws + plan.off_k);
-        a.checkpoints = reinterpret_cast<float*>(ws + plan.off_a);
-        a.scratch = reinterpret_cast<float*>(ws + plan.off_b);
-        a.slots = plan.slots;
+        const bool chunked = d.dtype == KDA_DTYPE_BF16;
+        if (chunked) {
+            a.states = ws + plan.off_a; a.sgrads = ws + plan.off_b; a.u = ws + plan.off_c; a.dx = ws + plan.off_d;
+            a.nv = kda::gdn_backward_nv(d.dv, (int64_t)num_seqs * d.hv, kda::device_cu_count());
+        } else {
+            a.checkpoints = reinterpret_cast<float*>(ws + plan.off_a);
+            a.scratch = reinterpret_cast<float*>(ws + plan.off_b);
+            a.slots = plan.slots;
+        }
         const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
         const std::vector<int32_t> order = longest_first(cu_seqlens_host, num_seqs);
         kda::GdnTable tab;
         hipError_t e = hipSuccess;
         for (int32_t from = 0; from < num_seqs && e == hipSuccess; from += a.num_seqs) {
             a.num_seqs = fill_table(tab, cu_seqlens_host, order, from);
-            e = kda::launch_gdn_backward_seq(a, tab, hs);
+            e = chunked ? kda::launch_gdn_backward_chunked(a, tab, hs) : kda::launch_gdn_backward_seq(a, tab, hs);
         }
         if (e == hipSuccess && a.parts) e = kda::launch_gdn_sum_parts(a, hs);
         if (e != hipSuccess) return fail(KDA_ERR_HIP, "kda_gdn_prefill_backward launch: %s", hipGetErrorString(e));

@@ -164,21 +164,24 @@ __device__ __forceinline__ f32x4 decay_col(const unsigned char* gv, int t, int s
     return d;
 }
 
-// Row fragments of one 16-token tile of a staged tensor, and the product of two of them:
-// lane (r, g) of tile_dot(X, Y) holds X_{4g+i} . Y_r
-template <int DK>
+// Row fragments of one 16-token tile of a staged tensor (fp16, or bf16 as given), and the
+// product of two of them: lane (r, g) of tile_dot(X, Y) holds X_{4g+i} . Y_r
+template <int DK, bool HALF = true>
 struct TileRows {
-    f16x8 v[DK / 32];
+    typedef std::conditional_t<HALF, f16x8, bf16x8> E8;
+    E8 v[DK / 32];
     __device__ __forceinline__ void load(const unsigned char* tile, int t, int r, int g) {
 #pragma unroll
-        for (int p = 0; p < DK / 32; ++p) v[p] = lds_ld<f16x8>(tile + (16 * t + r) * KeyTile<DK>::RS + 64 * p + 16 * g);
+        for (int p = 0; p < DK / 32; ++p) v[p] = lds_ld<E8>(tile + (16 * t + r) * KeyTile<DK>::RS + 64 * p + 16 * g);
     }
 };
-template <int DK>
-__device__ __forceinline__ f32x4 tile_dot(const TileRows<DK>& x, const TileRows<DK>& y) {
+__device__ __forceinline__ f32x4 mma32(f16x8 a, f16x8 b, f32x4 c) { return mfma32h(a, b, c); }
+__device__ __forceinline__ f32x4 mma32(bf16x8 a, bf16x8 b, f32x4 c) { return mfma32(a, b, c); }
+template <int DK, bool HALF>
+__device__ __forceinline__ f32x4 tile_dot(const TileRows<DK, HALF>& x, const TileRows<DK, HALF>& y) {
     f32x4 c = zero4();
 #pragma unroll
-    for (int p = 0; p < DK / 32; ++p) c = mfma32h(x.v[p], y.v[p], c);
+    for (int p = 0; p < DK / 32; ++p) c = mma32(x.v[p], y.v[p], c);
     return c;
 }
 
@@ -191,14 +194,14 @@ struct HalfState {
     float na[16], x[16];
 };
 constexpr int kHalfSteps = 6;  // of 15 in the first step: the phases it is split over come out even
-template <int DK>
+template <int DK, bool HALF>
 __device__ __forceinline__ HalfState half_columns(const unsigned char* Kt, const unsigned char* gv, unsigned char* sc, int half, int lane) {
     typedef InvScratch I;
     const int r = lane & 15, g = lane >> 4, t0 = 32 * half;
-    TileRows<DK> k0, k1;
+    TileRows<DK, HALF> k0, k1;
     k0.load(Kt, 2 * half, r, g);
     k1.load(Kt, 2 * half + 1, r, g);
-    f32x4 da = tile_dot<DK>(k0, k0), db = tile_dot<DK>(k1, k1), sub = tile_dot<DK>(k0, k1);
+    f32x4 da = tile_dot(k0, k0), db = tile_dot(k1, k1), sub = tile_dot(k0, k1);
     const f32x4 ba = lds_ld<f32x4>(gv + GateVec::BE + 4 * (t0 + 4 * g));
     const f32x4 bb = lds_ld<f32x4>(gv + GateVec::BE + 4 * (t0 + 16 + 4 * g));
     const float bs = lds_ld<float>(gv + GateVec::BE + 4 * (t0 + 16 + r));
@@ -228,9 +231,12 @@ __device__ __forceinline__ HalfState half_columns(const unsigned char* Kt, const
     invert16<0, kHalfSteps>(h.na, h.x);
     return h;
 }
-// Then the rest of it, the inverses' columns through the scratch, and the join.  rows[0]: row tile 0, columns 0..15; rows[1], rows[2]: row tile 1, columns
-// 0..15 and 16..31; lane (r, g) gets row r, columns 4g .. 4g+3.
-__device__ __forceinline__ void half_join(unsigned char* sc, HalfState& h, int lane, f32x4 (&rows)[3]) {
+// Then the rest of it and the join.  T: the fragments of the inverse's rows, rows[0]: row tile
+// 0, columns 0..15; rows[1], rows[2]: row tile 1, columns 0..15 and 16..31; lane (r, g) gets
+// row r, columns 4g .. 4g+3.  TRANSPOSED: those of its transpose, [0] and [1]: row tile 0,
+// columns 0..15 and 16..31; [2]: row tile 1, columns 16..31.
+template <bool TRANSPOSED>
+__device__ __forceinline__ void half_join(unsigned char* sc, HalfState& h, int lane, f32x4 (&T)[3]) {
     typedef InvScratch I;
     const int r = lane & 15, g = lane >> 4;
     invert16<kHalfSteps, 15>(h.na, h.x);
@@ -243,14 +249,32 @@ __device__ __forceinline__ void half_join(unsigned char* sc, HalfState& h, int l
     wave_lds_sync();
     f32x4 tb;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        rows[0][i] = lds_ld<float>(sc + I::COL * (4 * g + i) + 4 * r);
-        tb[i] = lds_ld<float>(sc + I::BLK + I::COL * (4 * g + i) + 4 * r);
+    for (int i = 0; i < 4; ++i) tb[i] = lds_ld<float>(sc + I::BLK + I::COL * (4 * g + i) + 4 * r);
+    // M = A_10 T_a (ta: its column fragment), then -T_b M, transposed by swapping the operands
+    const f32x4 ta = lds_ld<f32x4>(sc + I::COL * r + 16 * g);
+    const f32x4 m = Mma<float>::run(h.sub, ta, zero4());
+    if constexpr (TRANSPOSED) {
+        T[0] = ta;
+        T[1] = -Mma<float>::run(tb, m, zero4());
+        T[2] = lds_ld<f32x4>(sc + I::BLK + I::COL * r + 16 * g);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) T[0][i] = lds_ld<float>(sc + I::COL * (4 * g + i) + 4 * r);
+        T[1] = -Mma<float>::run(m, tb, zero4());
+        T[2] = tb;
     }
-    // M = A_10 T_a, then the transpose of -T_b M (its accumulator is a row fragment)
-    const f32x4 m = Mma<float>::run(h.sub, lds_ld<f32x4>(sc + I::COL * r + 16 * g), zero4());
-    rows[1] = -Mma<float>::run(m, tb, zero4());
-    rows[2] = tb;
 }
+
+// What the backward's launches pass on, per (chunk, value head), as pairs of bf16 (hi plane,
+// then lo plane), each plane [dv][*]: the state before the chunk and the gradient of the state
+// behind it over key channels, U and dX over the chunk's tokens (order: position 32s + 8g + 4h
+// + i holds token 32s + 16h + 4g + i, which is how a wave's registers hold them).
+struct BwdSlot {
+    __device__ static __forceinline__ int64_t index(int64_t start, int id, int len, int hv, int h, int c) {
+        return (start / kGC + id) * hv + (int64_t)h * ((len + kGC - 1) / kGC) + c;
+    }
+    static constexpr int64_t state(int dk, int dv) { return 2ll * dk * dv; }    // elements
+    static constexpr int64_t tokens(int dv) { return 2ll * kGC * dv; }
+};
 
 }  // namespace kda

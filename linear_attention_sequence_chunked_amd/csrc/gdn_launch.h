@@ -33,6 +33,8 @@ struct GdnPrefillArgs {
     float* final_state;          // may be null
     void* out;
     int nv;                      // value columns per workgroup
+    // the backward's states: each chunk's S and U as bf16 pairs, no outputs (both or neither)
+    void *save_states, *save_u;
 };
 
 constexpr int kGdnMaxTokens = 16;  // tokens per sequence of the recurrent form
@@ -65,6 +67,9 @@ struct GdnBackwardArgs {
     // token by token: states before every 16th token, and a scratch of 16 states per workgroup
     float *checkpoints, *scratch;
     int slots;                    // workgroups the scratch serves
+    // in chunks: per (chunk, value head) the states, their gradients, U and dX (gdn_chunk.h)
+    void *states, *sgrads, *u, *dx;
+    int nv;
 };
 
 struct AcceptArgs {
@@ -84,6 +89,8 @@ struct AcceptArgs {
 int gdn_recurrent_nv(int dv, int64_t pairs, int cu_count);
 // value columns per workgroup of the chunked prefill (gdn_plan.cpp)
 int gdn_prefill_nv(int dv, int64_t pairs, int cu_count);
+// value columns per workgroup of the backward's walks (gdn_plan.cpp)
+int gdn_backward_nv(int dv, int64_t pairs, int cu_count);
 // pieces the vocabulary of one sequence is cut into (gdn_plan.cpp)
 int accept_pieces(int64_t num_seqs, int64_t vocab, int cu_count);
 
@@ -91,6 +98,7 @@ hipError_t launch_gdn_recurrent(const GdnRecurrentArgs& a, hipStream_t stream);
 hipError_t launch_gdn_sequential(const GdnPrefillArgs& a, const GdnTable& t, hipStream_t stream);
 hipError_t launch_gdn_chunked(const GdnPrefillArgs& a, const GdnTable& t, hipStream_t stream);
 hipError_t launch_gdn_backward_seq(const GdnBackwardArgs& a, const GdnTable& t, hipStream_t stream);
+hipError_t launch_gdn_backward_chunked(const GdnBackwardArgs& a, const GdnTable& t, hipStream_t stream);
 hipError_t launch_gdn_sum_parts(const GdnBackwardArgs& a, hipStream_t stream);
 hipError_t launch_accept(const AcceptArgs& a, hipStream_t stream);
 

@@ -21,6 +21,11 @@ int gdn_prefill_nv(int dv, int64_t pairs, int cu_count) {
     return nv;
 }
 
+int gdn_backward_nv(int dv, int64_t pairs, int cu_count) {
+    // the walks have the narrow form alone
+    return pairs * (dv / 32) < cu_count ? 16 : 32;
+}
+
 int accept_pieces(int64_t num_seqs, int64_t vocab, int cu_count) {
     // Four workgroups per compute unit over the batch, but no piece below 2048 entries
     // (eight per thread) and at most 256 pieces (one partial sum per thread of the join).

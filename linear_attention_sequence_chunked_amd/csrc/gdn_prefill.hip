@@ -27,6 +27,8 @@
 //  * wide (64 or 128 columns): the chain waves (two column blocks each at 128) do the out
 //    wave's work on their own registers, and four producer waves stage in phase A and invert
 //    or form Gram tiles, two and two, in phase B; more waves would not have the registers.
+// SAVE (the backward's first launch, narrow): no outputs; in the out wave's place a save wave
+// stores each chunk's S and U as bf16 pairs.
 //
 // Precision.  Operands are fp16.  The products that make the state (K S, the solve, K^T U)
 // take their fp32 side as a pair hi + lo (22 bits): single operands would leave the fp32 state
@@ -43,10 +45,11 @@ namespace {
 
 constexpr float kPre = 8.f;  // v and the state are carried times this
 
-template <int DK, int NCB>
+template <int DK, int NCB, bool SAVE = false>
 struct GCfg {
     static constexpr int KB = DK / 16, KP = DK / 32, NV = 16 * NCB;
-    static constexpr bool NARROW = NCB <= 2;
+    static constexpr bool NARROW = NCB <= 2, OUT = !SAVE;
+    static_assert(NARROW || OUT, "states are saved by the narrow form");
     // two column blocks per chain wave at full width, so that an operand read from LDS serves
     // 32 columns; one otherwise (the shortest step)
     static constexpr int CPW = NCB >= 8 ? 2 : 1;
@@ -62,9 +65,10 @@ struct GCfg {
     static constexpr int M_T0 = 0, M_T1 = 4 * FR, M_A = 8 * FR, M_P = 12 * FR, M_SIZE = 18 * FR;
     // vectors over the chunk's tokens: e^G, beta e^G, kPre beta, e^{G_C - G}; e^{G_C}
     static constexpr int V_EG = 0, V_BE = 256, V_B = 512, V_ER = 768, V_GC = 1024, V_SIZE = 1040;
-    // operands for the out wave, per column block: S, then U
-    static constexpr int X_S = 0, X_U = KP * FR, X_SIZE = X_U + 2 * FR;
-    static constexpr int O_K = 0, O_Q = O_K + 2 * K::SIZE, O_V = O_Q + 2 * K::SIZE, O_M = O_V + 2 * V::SIZE,
+    // operands for the out (save) wave, per column block: S, then U; behind each its low half
+    static constexpr int XN = SAVE ? 2 : 1;
+    static constexpr int X_S = 0, X_U = XN * KP * FR, X_SIZE = X_U + XN * 2 * FR;
+    static constexpr int O_K = 0, O_Q = O_K + 2 * K::SIZE, O_V = O_Q + (OUT ? 2 * K::SIZE : 0), O_M = O_V + 2 * V::SIZE,
                          O_VEC = O_M + 2 * M_SIZE, O_G = O_VEC + 2 * V_SIZE, O_INV = O_G + 2 * GateVec::SIZE,
                          O_X = O_INV + 2 * InvScratch::SIZE, LDS_BYTES = O_X + (NARROW ? NCB * X_SIZE : 0);
     static_assert(LDS_BYTES <= 160 * 1024, "LDS budget");
@@ -79,6 +83,7 @@ struct PArgs {
     int64_t qs, ks, vs;
     int hk, hv, dv, slices, groups;
     float scale;
+    bf16 *save_s, *save_u;
     GdnTable tab;
 };
 
@@ -98,9 +103,9 @@ __device__ __forceinline__ void split8(f32x4 a, f32x4 b, f16x8& hi, f16x8& lo, f
     lo = cat8h(l0, l1);
 }
 
-template <int DK, int NCB>
-__global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(const PArgs a) {
-    typedef GCfg<DK, NCB> C;
+template <int DK, int NCB, bool SAVE>
+__global__ __launch_bounds__((GCfg<DK, NCB, SAVE>::THREADS)) void gdn_prefill_kernel(const PArgs a) {
+    typedef GCfg<DK, NCB, SAVE> C;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -139,7 +144,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         const int rows = min(kGC, len - kGC * c);
         const int64_t at = start + (int64_t)kGC * c;
         load_rows<C::K::PPT, DK / 8>(x.k, a.k + at * a.ks + (int64_t)hk * DK, a.ks, rows, st);
-        load_rows<C::K::PPT, DK / 8>(x.q, a.q + at * a.qs + (int64_t)hk * DK, a.qs, rows, st);
+        if constexpr (C::OUT) load_rows<C::K::PPT, DK / 8>(x.q, a.q + at * a.qs + (int64_t)hk * DK, a.qs, rows, st);
         load_rows<C::V::PPT, C::NV / 8>(x.v, a.v + at * a.vs + (int64_t)h * a.dv + col0, a.vs, rows, st);
         x.la = x.be = 0.f;
         if (wave == C::W_STAGE && lane < rows) {
@@ -150,7 +155,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
     auto stage = [&](const Staged& x, int c, auto CONVERT) {  // CONVERT: the rows are bf16 still
         unsigned char* Vt = buf(C::O_V, C::V::SIZE, c);
         store_key<DK, decltype(CONVERT)::value>(buf(C::O_K, C::K::SIZE, c), x.k, st);
-        store_key<DK, decltype(CONVERT)::value>(buf(C::O_Q, C::K::SIZE, c), x.q, st);
+        if constexpr (C::OUT) store_key<DK, decltype(CONVERT)::value>(buf(C::O_Q, C::K::SIZE, c), x.q, st);
 #pragma unroll
         for (int i = 0; i < C::V::PPT; ++i) {
             const int e = st + 256 * i;
@@ -173,11 +178,11 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
     };
     unsigned char* isc = smem + C::O_INV + (wave - C::W_INV) * InvScratch::SIZE;  // inverse waves
     auto columns = [&](int c) {
-        return half_columns<DK>(buf(C::O_K, C::K::SIZE, c), buf(C::O_G, GateVec::SIZE, c), isc, wave - C::W_INV, lane);
+        return half_columns<DK, true>(buf(C::O_K, C::K::SIZE, c), buf(C::O_G, GateVec::SIZE, c), isc, wave - C::W_INV, lane);
     };
     auto join = [&](HalfState& x, int c) {
         f32x4 rows[3];
-        half_join(isc, x, lane, rows);
+        half_join<false>(isc, x, lane, rows);
         unsigned char* d = buf(C::O_M, C::M_SIZE, c) + (wave == C::W_INV ? C::M_T0 : C::M_T1) + 16 * lane;
         const int at[3] = {0, C::FR, C::FR + 8};
 #pragma unroll
@@ -196,20 +201,22 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         const unsigned char* gv = buf(C::O_G, GateVec::SIZE, c);
         unsigned char* M = buf(C::O_M, C::M_SIZE, c);
         TileRows<DK> qt, ki;
-        qt.load(buf(C::O_Q, C::K::SIZE, c), it, r, g);
+        if constexpr (C::OUT) qt.load(buf(C::O_Q, C::K::SIZE, c), it, r, g);
         if constexpr (it >= 2 && decltype(J0)::value < 2) ki.load(Kt, it, r, g);
         unroll<decltype(J0)::value, decltype(J1)::value>([&](auto JT) {
             constexpr int jt = decltype(JT)::value;
             TileRows<DK> kj;
             kj.load(Kt, jt, r, g);
             const f32x4 d = decay_row(gv, 16 * it + r, 16 * jt + 4 * g);
-            f32x4 p = tile_dot<DK>(kj, qt);
+            if constexpr (C::OUT) {
+                f32x4 p = tile_dot(kj, qt);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = it > jt || 4 * g + i <= r ? d[i] * p[i] : 0.f;
-            // P: block (rows 32 (it / 2), columns 32 (jt / 2)), row tile it % 2
-            lds_st(M + C::M_P + (2 * (it / 2 + jt / 2) + it % 2) * C::FR + 16 * lane + 8 * (jt % 2), to_h4(p));
+                for (int i = 0; i < 4; ++i) p[i] = it > jt || 4 * g + i <= r ? d[i] * p[i] : 0.f;
+                // P: block (rows 32 (it / 2), columns 32 (jt / 2)), row tile it % 2
+                lds_st(M + C::M_P + (2 * (it / 2 + jt / 2) + it % 2) * C::FR + 16 * lane + 8 * (jt % 2), to_h4(p));
+            }
             if constexpr (it / 2 != jt / 2) {
-                const f32x4 x = tile_dot<DK>(kj, ki);
+                const f32x4 x = tile_dot(kj, ki);
                 const float nb = -lds_ld<float>(gv + GateVec::BE + 4 * (16 * it + r));
                 f16x4 hi, lo;
                 split4h(nb * (d * x), hi, lo, m1);
@@ -231,6 +238,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         else gram_row(i3, i0, i2, c);
     };
     auto gram_second = [&](int n, int c) {
+        if constexpr (!C::OUT) return;
         if (n == 0) {
             gram_row(i2, i2, i3, c);
             gram_row(i1, i0, i2, c);
@@ -271,7 +279,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
 #pragma unroll
             for (int i = 0; i < C::K::PPT; ++i) {
                 y.k[i] = staged8<true>(y.k[i]);
-                y.q[i] = staged8<true>(y.q[i]);
+                if constexpr (C::OUT) y.q[i] = staged8<true>(y.q[i]);
             }
         };
         if (nch > 0) load(x[0], 0);
@@ -323,6 +331,46 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, to_bf4(oscale * o)), rs, 2 * (r * os + 4 * g) + 2 * col,
                                               32 * t * os, 0);
     };
+    if constexpr (SAVE) {
+        if (wave == C::W_OUT) {
+            // eight fp16 pairs (times kPre) of lane's column and channels or tokens -> bf16 pairs
+            auto put = [&](bf16* hi, int64_t plane, const unsigned char* x, int lo_off) {
+                const f16x8 h = lds_ld<f16x8>(x), l = lds_ld<f16x8>(x + lo_off);
+                f32x4 v[2];
+                bf16x4 bh[2], bl[2];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i / 4][i % 4] = ((float)h[i] + (float)l[i]) * (1.f / kPre);
+                split4(v[0], bh[0], bl[0]);
+                split4(v[1], bh[1], bl[1]);
+                *reinterpret_cast<bf16x8*>(hi) = cat8(bh[0], bh[1]);
+                *reinterpret_cast<bf16x8*>(hi + plane) = cat8(bl[0], bl[1]);
+            };
+            const int64_t slot = BwdSlot::index(start, a.tab.id[si], len, a.hv, h, 0);
+            auto save_u = [&](int c) {
+#pragma unroll
+                for (int cb = 0; cb < NCB; ++cb)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        put(a.save_u + (slot + c) * BwdSlot::tokens(a.dv) + (int64_t)(col0 + 16 * cb + r) * kGC + 32 * s + 8 * g,
+                            (int64_t)kGC * a.dv, smem + C::O_X + cb * C::X_SIZE + C::X_U + s * C::FR + 16 * lane, 2 * C::FR);
+            };
+            for (int c = 0; c <= nch; ++c) {
+                if (c > 1) save_u(c - 2);
+                lds_barrier();
+                if (c > 0) {
+#pragma unroll
+                    for (int cb = 0; cb < NCB; ++cb)
+#pragma unroll
+                        for (int p = 0; p < KP; ++p)
+                            put(a.save_s + (slot + c - 1) * BwdSlot::state(DK, a.dv) + (int64_t)(col0 + 16 * cb + r) * DK + 32 * p + 8 * g,
+                                (int64_t)DK * a.dv, smem + C::O_X + cb * C::X_SIZE + C::X_S + p * C::FR + 16 * lane, KP * C::FR);
+                }
+                lds_barrier();
+            }
+            if (nch > 0) save_u(nch - 1);
+            return;
+        }
+    }
     if (C::NARROW && wave == C::W_OUT) {
         f32x4 O[NCB][4];
         auto done = [&](int c) {
@@ -433,6 +481,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
 #pragma unroll
             for (int cb = 0; cb < CPW; ++cb) split8(S[cb][2 * p], S[cb][2 * p + 1], sh[cb], sl[cb], m1);
             if constexpr (C::NARROW) lds_st(xw + C::X_S + p * C::FR, sh[0]);
+            if constexpr (SAVE) lds_st(xw + C::X_S + (KP + p) * C::FR, sl[0]);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -569,8 +618,15 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
         load_cols(kt[0], 1, 0);
         e0 = tokens(C::V_ER, 32);
         e1 = tokens(C::V_ER, 48);
+        if constexpr (SAVE) {
+            f16x8 l1;
+            split8(U[0][2], U[0][3], uh[0][1], l1, m1);
+            lds_st(xw + C::X_U + 2 * C::FR, ul[0]);
+            lds_st(xw + C::X_U + 3 * C::FR, l1);
+        } else {
 #pragma unroll
-        for (int cb = 0; cb < CPW; ++cb) uh[cb][1] = to_h8(U[cb][2], U[cb][3]);
+            for (int cb = 0; cb < CPW; ++cb) uh[cb][1] = to_h8(U[cb][2], U[cb][3]);
+        }
         if constexpr (C::NARROW) {
             lds_st(xw + C::X_U, uh[0][0]);
             lds_st(xw + C::X_U + C::FR, uh[0][1]);
@@ -601,29 +657,34 @@ __global__ __launch_bounds__((GCfg<DK, NCB>::THREADS)) void gdn_prefill_kernel(c
     }
 }
 
-template <int DK, int NCB>
+template <int DK, int NCB, bool SAVE>
 hipError_t launch(const GdnPrefillArgs& p, const GdnTable& tab, hipStream_t st) {
-    typedef GCfg<DK, NCB> C;
+    typedef GCfg<DK, NCB, SAVE> C;
     PArgs a;
     a.q = (const bf16*)p.q; a.k = (const bf16*)p.k; a.v = (const bf16*)p.v;
     a.la = p.log_alpha; a.be = p.beta; a.S0 = p.initial_state; a.Sf = p.final_state; a.out = (bf16*)p.out;
     a.qs = p.d.qs; a.ks = p.d.ks; a.vs = p.d.vs; a.hk = p.d.hk; a.hv = p.d.hv; a.dv = p.d.dv;
     a.slices = p.d.dv / C::NV; a.groups = p.num_seqs * p.d.hv; a.scale = p.d.scale; a.tab = tab;
+    a.save_s = (bf16*)p.save_states; a.save_u = (bf16*)p.save_u;
     const int64_t blocks = ((int64_t)a.groups + 7) / 8 * 8 * a.slices;
-    hipError_t e = hipFuncSetAttribute((const void*)gdn_prefill_kernel<DK, NCB>,
+    hipError_t e = hipFuncSetAttribute((const void*)gdn_prefill_kernel<DK, NCB, SAVE>,
                                        hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS_BYTES);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gdn_prefill_kernel<DK, NCB>), dim3((unsigned)blocks), dim3(C::THREADS), C::LDS_BYTES, st, a);
+    hipLaunchKernelGGL((gdn_prefill_kernel<DK, NCB, SAVE>), dim3((unsigned)blocks), dim3(C::THREADS), C::LDS_BYTES, st, a);
     return hipGetLastError();
 }
 
 template <int DK>
 hipError_t launch_nv(const GdnPrefillArgs& p, const GdnTable& tab, hipStream_t st) {
+    if (p.save_states) {
+        if (p.nv == 16) return launch<DK, 1, true>(p, tab, st);
+        return p.nv == 32 ? launch<DK, 2, true>(p, tab, st) : hipErrorInvalidValue;
+    }
     switch (p.nv) {
-        case 16: return launch<DK, 1>(p, tab, st);
-        case 32: return launch<DK, 2>(p, tab, st);
-        case 64: return launch<DK, 4>(p, tab, st);
-        case 128: return launch<DK, 8>(p, tab, st);
+        case 16: return launch<DK, 1, false>(p, tab, st);
+        case 32: return launch<DK, 2, false>(p, tab, st);
+        case 64: return launch<DK, 4, false>(p, tab, st);
+        case 128: return launch<DK, 8, false>(p, tab, st);
     }
     return hipErrorInvalidValue;
 }
