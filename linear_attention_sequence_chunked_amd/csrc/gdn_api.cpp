@@ -282,7 +282,7 @@ kda_status kda_gdn_chunk_prefill(const kda_gdn_params* params, const void* q, co
         a.q = q; a.k = k; a.v = v; a.log_alpha = log_alpha; a.beta = beta;
         a.initial_state = initial_state; a.final_state = final_state; a.out = out;
         const bool chunked = d.dtype == KDA_DTYPE_BF16;
-        a.nv = chunked ? kda::gdn_prefill_nv(d.dv, pairs, cus) : kda::gdn_recurrent_nv(d.dv, pairs, cus);
+        a.nv = chunked ? kda::gdn_prefill_nv(d.dv, pairs, cus) : kda::gdn_recurrent_nv(d.dv, pairs, 2, cus);
         const std::vector<int32_t> order = longest_first(cu_seqlens_host, num_seqs);
         kda::GdnTable tab;
         for (int32_t from = 0; from < num_seqs; from += a.num_seqs) {
@@ -338,7 +338,7 @@ kda_status kda_gdn_recurrent(const kda_gdn_params* params, const void* q, const 
     a.num_seqs = num_seqs; a.num_tokens = num_tokens; a.num_slots = num_slots;
     a.q = q; a.k = k; a.v = v; a.log_alpha = log_alpha; a.beta = beta; a.steps = steps;
     a.state_indices = state_indices; a.state = state; a.update = update_state != 0; a.out = out;
-    a.nv = kda::gdn_recurrent_nv(d.dv, (int64_t)num_seqs * d.hv, kda::device_cu_count());
+    a.nv = kda::gdn_recurrent_nv(d.dv, (int64_t)num_seqs * d.hv, num_tokens, kda::device_cu_count());
     const hipError_t e = kda::launch_gdn_recurrent(a, reinterpret_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(KDA_ERR_HIP, "kda_gdn_recurrent launch: %s", hipGetErrorString(e));
     return kda::ok();

@@ -86,7 +86,7 @@ struct AcceptArgs {
 };
 
 // value columns per workgroup of the token-by-token kernel (gdn_plan.cpp)
-int gdn_recurrent_nv(int dv, int64_t pairs, int cu_count);
+int gdn_recurrent_nv(int dv, int64_t pairs, int tokens, int cu_count);
 // value columns per workgroup of the chunked prefill (gdn_plan.cpp)
 int gdn_prefill_nv(int dv, int64_t pairs, int cu_count);
 // value columns per workgroup of the backward's walks (gdn_plan.cpp)

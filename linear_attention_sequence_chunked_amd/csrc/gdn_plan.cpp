@@ -6,11 +6,15 @@
 
 namespace kda {
 
-int gdn_recurrent_nv(int dv, int64_t pairs, int cu_count) {
-    // Whole rows of the state per workgroup once the (sequence, head) pairs give every
-    // compute unit two of them; 32 columns (128-byte row segments, still whole cache lines)
-    // below that, so that a small batch spreads over more compute units.
-    return pairs >= 2 * (int64_t)cu_count ? dv : 32;
+int gdn_recurrent_nv(int dv, int64_t pairs, int tokens, int cu_count) {
+    // Below two (sequence, head) pairs per compute unit, 32 columns (128-byte row segments,
+    // still whole cache lines) spread a small batch over more units: one token of one sequence
+    // with 32 heads takes 4.4 us, 5.9 us with whole rows.  Above, one token takes whole rows of
+    // the state per workgroup (256 x 32 states of 128 x 128: 162 us, 209 us in halves), several
+    // tokens, which keep the state in registers for long, halves of them (96 x 32 states, 4
+    // tokens: 59 us, 67 us with whole rows).
+    if (pairs < 2 * (int64_t)cu_count) return 32;
+    return tokens == 1 ? dv : 64;
 }
 
 int gdn_prefill_nv(int dv, int64_t pairs, int cu_count) {
@@ -27,11 +31,12 @@ int gdn_backward_nv(int dv, int64_t pairs, int cu_count) {
 }
 
 int accept_pieces(int64_t num_seqs, int64_t vocab, int cu_count) {
-    // Four workgroups per compute unit over the batch, but no piece below 2048 entries
-    // (eight per thread) and at most 256 pieces (one partial sum per thread of the join).
-    const int64_t want = (4 * (int64_t)cu_count + num_seqs - 1) / std::max<int64_t>(num_seqs, 1);
-    const int64_t most = std::min<int64_t>(256, (vocab + 2047) / 2048);
-    return (int)std::max<int64_t>(1, std::min(want, most));
+    // Pieces of about 4096 entries, which is what the join scans in one go; shorter ones (2048
+    // at the least, eight entries per thread) while the batch gives the card too few
+    // workgroups; at most 256 (one partial sum per thread of the join).
+    const int64_t fill = (4 * (int64_t)cu_count + num_seqs - 1) / std::max<int64_t>(num_seqs, 1);
+    const int64_t want = std::max((vocab + 4095) / 4096, std::min(fill, (vocab + 2047) / 2048));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(want, 256));
 }
 
 }  // namespace kda

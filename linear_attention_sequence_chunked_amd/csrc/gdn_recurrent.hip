@@ -11,21 +11,24 @@
 // operand, read once and written once whatever the number of tokens; HBM-bound.  The
 // sequential prefill (any length, the form of 32-bit inputs): the state stays in registers
 // for the whole sequence and the tokens stream through LDS in blocks of 16, one barrier per
-// token; bound by that barrier and the two reductions (see the table in launch below).
+// token; bound by that barrier and the two reductions (0.7 us a token at 64 x 128).
 //
 // A workgroup of four waves owns NV value columns of one state.  Thread t holds columns
-// 4 (t % COLG) .. +3 of RPT consecutive rows, so a row of the slice is read and written by
-// COLG consecutive threads as one contiguous segment and a thread's k and q come from LDS
-// as 16-byte reads.  Everything is fp32; outputs are rounded once to their type.
+// 4 (t % COLG) .. +3 of rows rg + ROWG i (rg = t / COLG): a row of the slice is read and written
+// by COLG consecutive threads as one contiguous segment, and the workgroup's accesses of one i
+// are one contiguous stretch of the state.  k and q lie in LDS in the order of the threads'
+// rows, so a thread reads its own as 16-byte pieces.  TB tokens are staged at a time: four for
+// the short steps, whose LDS then lets more workgroups share a compute unit and keep its loads
+// in flight.  Everything is fp32; outputs are rounded once to their type.
 #include "gdn_launch.h"
 #include "kda_device.h"
 #include "kda_launch.h"
+#include "kda_mfma.h"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int TB = 16;  // tokens staged at a time
 
 struct RecArgs {
     const void *q, *k, *v;
@@ -49,19 +52,26 @@ __device__ inline f32x4 load4f(const bf16* p) {
     return __builtin_convertvector(*reinterpret_cast<const bf16x4*>(p), f32x4);
 }
 
-template <typename T, int DK, int DV, int NV>
+// a x + c, fused as written: the kernels below form the same bits from the same state and token
+__device__ inline f32x4 fma4(float a, f32x4 x, f32x4 c) {
+    return f32x4{fmaf(a, x[0], c[0]), fmaf(a, x[1], c[1]), fmaf(a, x[2], c[2]), fmaf(a, x[3], c[3])};
+}
+
+template <int DK, int NV, int TB>
 struct Tile {
     static constexpr int COLG = NV / 4, ROWG = kThreads / COLG, RPT = DK / ROWG;
-    static constexpr int QV = TB * DK / 4 / kThreads;  // 16-byte pieces of q (and k) per thread
-    static constexpr int VV = TB * NV / 4 / kThreads > 0 ? TB * NV / 4 / kThreads : 1;
+    static constexpr int QV = (TB * DK / 4 + kThreads - 1) / kThreads;  // 16-byte pieces of q (and k) per thread
+    static constexpr int VV = (TB * NV / 4 + kThreads - 1) / kThreads;
     static_assert(DK % ROWG == 0 && RPT % 2 == 0, "shape");
+    // place of a row's k and q in LDS
+    static __device__ constexpr int place(int row) { return row % ROWG * RPT + row / ROWG; }
 };
 
 // The tokens' rows on their way from memory to LDS: loaded before a block of tokens is
 // worked on, stored after it.
-template <typename T, int DK, int DV, int NV>
+template <typename T, int DK, int DV, int NV, int TB>
 struct Stage {
-    using L = Tile<T, DK, DV, NV>;
+    using L = Tile<DK, NV, TB>;
     f32x4 q[L::QV], k[L::QV], v[L::VV];
     float g, b;
     __device__ void load(const RecArgs& A, int64_t row0, int n, int hk, int hv, int col0) {
@@ -91,10 +101,10 @@ struct Stage {
 
 // one sequence's tokens from row0 on; `advance` tokens move the stored state (to Sout),
 // outputs are written where `out` is given
-template <typename T, int DK, int DV, int NV>
+template <typename T, int DK, int DV, int NV, int TB>
 __device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t row0, int n,
                      int advance, T* out, int head, int col0, bool skip_check, int slot_seq) {
-    using L = Tile<T, DK, DV, NV>;
+    using L = Tile<DK, NV, TB>;
     __shared__ __attribute__((aligned(16))) float s_k[TB][DK], s_q[TB][DK], s_v[TB][NV];
     __shared__ float s_a[TB], s_b[TB], s_kq[TB];
     __shared__ f32x4 s_red[2][4][L::COLG][2];
@@ -103,11 +113,12 @@ __device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t ro
 
     // the state's loads first: the long-latency part of a step
     f32x4 s[L::RPT];
-    const int64_t at = (int64_t)(rg * L::RPT) * DV + col0 + 4 * cg;
+    const int64_t at = (int64_t)rg * DV + col0 + 4 * cg;
+    constexpr int STEP = L::ROWG * DV;
 #pragma unroll
     for (int i = 0; i < L::RPT; ++i)
-        s[i] = Sin ? *reinterpret_cast<const f32x4*>(Sin + at + i * DV) : zero4();
-    Stage<T, DK, DV, NV> st;
+        s[i] = Sin ? *reinterpret_cast<const f32x4*>(Sin + at + i * STEP) : zero4();
+    Stage<T, DK, DV, NV, TB> st;
     st.load(A, row0, min(n, TB), hk, head, col0);
     bool twice = false;  // an earlier row of this call names the same slot
     if (skip_check) {
@@ -125,7 +136,7 @@ __device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t ro
         // non-temporal: the state is not read again by this call
 #pragma unroll
         for (int i = 0; i < L::RPT; ++i)
-            __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(Sout + at + i * DV));
+            __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(Sout + at + i * STEP));
     };
     if (advance == 0 && Sout != Sin) put();
     for (int t0 = 0; t0 < n; t0 += TB) {
@@ -134,8 +145,13 @@ __device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t ro
 #pragma unroll
         for (int i = 0; i < L::QV; ++i) {
             const int e = t + kThreads * i, r = e / (DK / 4), c = 4 * (e % (DK / 4));
-            *reinterpret_cast<f32x4*>(&s_k[r][c]) = st.k[i];
-            *reinterpret_cast<f32x4*>(&s_q[r][c]) = st.q[i] * A.scale;
+            if (r < TB) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    s_k[r][L::place(c + x)] = st.k[i][x];
+                    s_q[r][L::place(c + x)] = st.q[i][x] * A.scale;
+                }
+            }
         }
 #pragma unroll
         for (int i = 0; i < L::VV; ++i) {
@@ -150,19 +166,19 @@ __device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t ro
         if (t0 + TB < n) st.load(A, row0 + t0 + TB, min(n - t0 - TB, TB), hk, head, col0);
         if (out) {  // k . (scale q) of every token: 16 lanes each
             float kq = 0.f;
+            const int tok = t / 16 % TB;
 #pragma unroll
-            for (int c = 0; c < DK / 16; ++c)
-                kq += s_k[t / 16][t % 16 + 16 * c] * s_q[t / 16][t % 16 + 16 * c];
+            for (int c = 0; c < DK / 16; ++c) kq = fmaf(s_k[tok][L::place(t % 16 + 16 * c)], s_q[tok][L::place(t % 16 + 16 * c)], kq);
 #pragma unroll
             for (int off = 8; off >= 1; off >>= 1) kq += __shfl_xor(kq, off);
-            if (t % 16 == 0) s_kq[t / 16] = kq;  // read behind the next barrier
+            if (t % 16 == 0 && t / 16 < TB) s_kq[tok] = kq;  // read behind the next barrier
         }
         for (int j = 0; j < m; ++j) {
             f32x4 w = zero4(), b = zero4();
 #pragma unroll
             for (int i = 0; i < L::RPT; ++i) {
-                w += s[i] * s_k[j][rg * L::RPT + i];
-                b += s[i] * s_q[j][rg * L::RPT + i];
+                w = fma4(s_k[j][rg * L::RPT + i], s[i], w);
+                b = fma4(s_q[j][rg * L::RPT + i], s[i], b);
             }
 #pragma unroll
             for (int off = L::COLG; off < 64; off <<= 1) {
@@ -182,12 +198,12 @@ __device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t ro
             b = (s_red[j & 1][0][cg][1] + s_red[j & 1][1][cg][1]) +
                 (s_red[j & 1][2][cg][1] + s_red[j & 1][3][cg][1]);
             const float a = s_a[j];
-            const f32x4 u = s_b[j] * (*reinterpret_cast<const f32x4*>(&s_v[j][4 * cg]) - a * w);
+            const f32x4 u = s_b[j] * fma4(-a, w, *reinterpret_cast<const f32x4*>(&s_v[j][4 * cg]));
 #pragma unroll
-            for (int i = 0; i < L::RPT; ++i) s[i] = a * s[i] + s_k[j][rg * L::RPT + i] * u;
+            for (int i = 0; i < L::RPT; ++i) s[i] = fma4(s_k[j][rg * L::RPT + i], u, a * s[i]);
             if (out && rg == 0)
                 store4(out + (row0 + t0 + j) * (int64_t)A.hv * DV + (int64_t)head * DV + col0 + 4 * cg,
-                       Mma<T>::pack(a * b + s_kq[j] * u));
+                       Mma<T>::pack(fma4(s_kq[j], u, a * b)));
             if (t0 + j + 1 == advance) {
                 put();
                 if (!out) return;  // (the whole workgroup: advance is the same for all)
@@ -196,8 +212,8 @@ __device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t ro
     }
 }
 
-template <typename T, int DK, int DV, int NV>
-__global__ __launch_bounds__(kThreads) void step_kernel(const RecArgs A) {
+template <typename T, int DK, int DV, int NV, int TB>
+__global__ __launch_bounds__(kThreads, TB <= 4 ? 4 : 3) void step_kernel(const RecArgs A) {
     constexpr int SL = DV / NV;
     const int64_t pair = blockIdx.x / SL;
     const int n = (int)(pair / A.hv), head = (int)(pair % A.hv), col0 = NV * (int)(blockIdx.x % SL);
@@ -215,7 +231,97 @@ __global__ __launch_bounds__(kThreads) void step_kernel(const RecArgs A) {
     if (A.update && A.steps) adv = min(max(A.steps[n], 0), A.num_tokens);
     if (adv == 0 && !out) return;
     float* S = A.state + ((int64_t)slot * A.hv + head) * (int64_t)(DK * DV);
-    walk<T, DK, DV, NV>(A, S, S, row0, A.num_tokens, adv, out, head, col0, A.update && A.slots, n);
+    walk<T, DK, DV, NV, TB>(A, S, S, row0, A.num_tokens, adv, out, head, col0, A.update && A.slots, n);
+}
+
+// One token per sequence, the decode step: the same arithmetic in the same order as walk's, with
+// nothing in registers but the state and what a row needs.  The token's loads are issued before
+// the state's and the barriers order LDS alone, so k, q and the repeated-slot check are done
+// while the state is on its way.
+template <typename T, int DK, int DV, int NV>
+__global__ __launch_bounds__(kThreads, 4) void decode_kernel(const RecArgs A) {
+    using L = Tile<DK, NV, 1>;
+    constexpr int SL = DV / NV, STEP = L::ROWG * DV;
+    __shared__ __attribute__((aligned(16))) float s_k[DK], s_q[DK];
+    __shared__ f32x4 s_red[4][L::COLG][2];
+    __shared__ int s_twice[4];
+    const int t = threadIdx.x, cg = t % L::COLG, rg = t / L::COLG, wave = t / 64, lane = t % 64;
+    const int pair = blockIdx.x / SL, n = pair / A.hv, head = pair % A.hv, col0 = NV * (int)(blockIdx.x % SL);
+    const int hk = head / (A.hv / A.hk);
+    T* out = A.out ? (T*)A.out + (int64_t)pair * DV + col0 : nullptr;
+    const int slot = A.slots ? A.slots[n] : n;
+    int adv = A.update;
+    if (A.update && A.steps) adv = A.steps[n] > 0;
+    const bool padded = slot < 0 || slot >= A.num_slots;
+    if (padded || (!adv && !out)) {
+        if (padded && out && t < L::COLG) store4(out + 4 * t, Mma<T>::pack(zero4()));
+        return;
+    }
+    const bool check = A.update && A.slots;
+    const int other = check && t < n ? A.slots[t] : -1;  // (the slot itself is not negative)
+    float kv = 0.f, qv = 0.f;
+    if (t < DK) {
+        kv = to_f32(((const T*)A.k)[n * A.ks + (int64_t)hk * DK + t]);
+        qv = A.scale * to_f32(((const T*)A.q)[n * A.qs + (int64_t)hk * DK + t]);
+    }
+    const f32x4 v = load4f((const T*)A.v + n * A.vs + (int64_t)head * DV + col0 + 4 * cg);
+    const float la = A.la[pair], be = A.be[pair];
+    float* S = A.state + ((int64_t)slot * A.hv + head) * (int64_t)(DK * DV) + rg * DV + col0 + 4 * cg;
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4 s[L::RPT];
+#pragma unroll
+    for (int i = 0; i < L::RPT; ++i) s[i] = *reinterpret_cast<const f32x4*>(S + i * STEP);
+    __builtin_amdgcn_sched_barrier(0);
+    if (t < DK) {
+        s_k[t] = kv;
+        s_q[t] = qv;
+    }
+    bool twice = other == slot;
+    if (check)
+        for (int j = t + kThreads; j < n; j += kThreads) twice |= A.slots[j] == slot;
+    const bool any = __ballot(twice) != 0;
+    if (lane == 0) s_twice[wave] = any;
+    lds_barrier();
+    if (s_twice[0] | s_twice[1] | s_twice[2] | s_twice[3]) {  // a repeated slot: a padded row
+        if (out && rg == 0) store4(out + 4 * cg, Mma<T>::pack(zero4()));
+        return;
+    }
+    const float a = expf(la);
+    float kq = 0.f;  // k . (scale q), summed as walk does
+    if (wave == 0) {
+#pragma unroll
+        for (int c = 0; c < DK / 16; ++c) kq = fmaf(s_k[t % 16 + 16 * c], s_q[t % 16 + 16 * c], kq);
+#pragma unroll
+        for (int off = 8; off >= 1; off >>= 1) kq += __shfl_xor(kq, off);
+    }
+    f32x4 w = zero4(), b = zero4();
+#pragma unroll
+    for (int i = 0; i < L::RPT; ++i) {
+        w = fma4(s_k[rg + L::ROWG * i], s[i], w);
+        b = fma4(s_q[rg + L::ROWG * i], s[i], b);
+    }
+#pragma unroll
+    for (int off = L::COLG; off < 64; off <<= 1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            w[c] += __shfl_xor(w[c], off);
+            b[c] += __shfl_xor(b[c], off);
+        }
+    }
+    if (lane < L::COLG) {
+        s_red[wave][lane][0] = w;
+        s_red[wave][lane][1] = b;
+    }
+    lds_barrier();
+    w = (s_red[0][cg][0] + s_red[1][cg][0]) + (s_red[2][cg][0] + s_red[3][cg][0]);
+    b = (s_red[0][cg][1] + s_red[1][cg][1]) + (s_red[2][cg][1] + s_red[3][cg][1]);
+    const f32x4 u = be * fma4(-a, w, v);
+    if (adv) {
+#pragma unroll
+        for (int i = 0; i < L::RPT; ++i)
+            __builtin_nontemporal_store(fma4(s_k[rg + L::ROWG * i], u, a * s[i]), reinterpret_cast<f32x4*>(S + i * STEP));
+    }
+    if (out && rg == 0) store4(out + 4 * cg, Mma<T>::pack(fma4(kq, u, a * b)));  // (wave 0)
 }
 
 template <typename T, int DK, int DV, int NV>
@@ -224,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void seq_kernel(const RecArgs A, const Gd
     const int64_t pair = blockIdx.x / SL;
     const int i = (int)(pair / A.hv), head = (int)(pair % A.hv), col0 = NV * (int)(blockIdx.x % SL);
     const int64_t ss = ((int64_t)tab.id[i] * A.hv + head) * (int64_t)(DK * DV);
-    walk<T, DK, DV, NV>(A, A.S0 ? A.S0 + ss : nullptr, A.Sf ? A.Sf + ss : nullptr, tab.start[i],
+    walk<T, DK, DV, NV, 16>(A, A.S0 ? A.S0 + ss : nullptr, A.Sf ? A.Sf + ss : nullptr, tab.start[i],
                         tab.len[i], tab.len[i], (T*)A.out, head, col0, false, 0);
 }
 
@@ -233,7 +339,7 @@ template <typename F>
 hipError_t dispatch(const GdnDims& d, int nv, F&& f) {
     auto nvs = [&](auto t, auto dk, auto dv) {
         if (nv == 32) return f(t, dk, dv, std::integral_constant<int, 32>{});
-        return f(t, dk, dv, dv);
+        return f(t, dk, dv, std::integral_constant<int, 64>{});
     };
     auto dvs = [&](auto t, auto dk) {
         if (d.dv == 128) return nvs(t, dk, std::integral_constant<int, 128>{});
@@ -262,9 +368,16 @@ hipError_t launch_gdn_recurrent(const GdnRecurrentArgs& a, hipStream_t stream) {
     const int64_t blocks = (int64_t)a.num_seqs * a.d.hv * (a.d.dv / a.nv);
     if (blocks == 0) return hipSuccess;
     return dispatch(a.d, a.nv, [&](auto t, auto dk, auto dv, auto nv) {
-        hipLaunchKernelGGL((step_kernel<decltype(t), decltype(dk)::value, decltype(dv)::value,
-                                        decltype(nv)::value>),
-                           dim3((unsigned)blocks), dim3(kThreads), 0, stream, r);
+        using T = decltype(t);
+        constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value, NV = decltype(nv)::value;
+        if (a.num_tokens == 1 && a.nv == DV)  // whole rows
+            hipLaunchKernelGGL((decode_kernel<T, DK, DV, DV>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, r);
+        else if (a.num_tokens == 1)
+            hipLaunchKernelGGL((decode_kernel<T, DK, DV, NV>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, r);
+        else if (a.num_tokens <= 4)
+            hipLaunchKernelGGL((step_kernel<T, DK, DV, NV, 4>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, r);
+        else
+            hipLaunchKernelGGL((step_kernel<T, DK, DV, NV, 16>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, r);
         return hipGetLastError();
     });
 }

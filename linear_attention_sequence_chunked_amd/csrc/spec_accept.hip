@@ -13,8 +13,9 @@
 //
 // Bound by reading one row of p and one of q per sequence; everything else is latency.  The
 // vocabulary is cut into pieces, so that one sequence also spreads over the card: a first
-// launch sums each piece, a second finds the piece that holds the draw from the sums (in
-// piece order: the same result whatever ran first) and scans that piece alone.
+// launch finds the kept drafts and sums each piece, a second finds the piece that holds the
+// draw from the sums (in piece order: the same result whatever ran first) and scans that piece
+// alone.
 #include "gdn_launch.h"
 #include "kda_device.h"
 #include "kda_launch.h"
@@ -101,17 +102,57 @@ __device__ void row_of(const AcceptArgs& A, int n, const Row& R, const T*& p, co
     }
 }
 
+// Sixteen bytes of a row from entry i on (any alignment of the entries' own size), as fp64
+template <typename T>
+struct Packed {
+    static constexpr int N = 16 / sizeof(T);
+    T v[N];
+} __attribute__((packed, aligned(sizeof(T))));
+
+// the weights of entries i .. i+N-1, all inside the row: r (and p, where given)
+template <typename T>
+__device__ inline void weights16(const T* p, const T* q, int64_t i, int64_t certain, double (&r)[Packed<T>::N], double (&pp)[Packed<T>::N]) {
+    constexpr int N = Packed<T>::N;
+    const Packed<T> a = *reinterpret_cast<const Packed<T>*>(p + i);
+    Packed<T> b;
+    if (q) b = *reinterpret_cast<const Packed<T>*>(q + i);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const double pv = to_f32(a.v[j]);
+        pp[j] = pv > 0.0 ? pv : 0.0;
+        r[j] = pp[j];
+        if (q) {
+            const double d = pv - (double)to_f32(b.v[j]);
+            r[j] = d > 0.0 ? d : 0.0;  // NaN counts as nothing
+        }
+        if (i + j == certain) r[j] = 0.0;
+    }
+}
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void sum_kernel(const AcceptArgs A) {
+    constexpr int N = Packed<T>::N;
     __shared__ double s_sum[4][2];
     const int n = blockIdx.x / A.pieces, piece = blockIdx.x % A.pieces;
     const Row R = find_row<T>(A, n);
     const T *p, *q;
     int64_t certain;
     row_of(A, n, R, p, q, certain);
+    if (piece == 0 && threadIdx.x == 0) A.accepted[n] = R.kept;
     const int64_t lo = piece * A.piece, hi = min(lo + A.piece, A.vocab);
     double sr = 0.0, sp = 0.0;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+    const int64_t whole = (hi - lo) / (N * kThreads) * (N * kThreads);
+#pragma unroll 2
+    for (int64_t i = lo + N * threadIdx.x; i < lo + whole; i += N * kThreads) {
+        double r[N], pp[N];
+        weights16(p, q, i, certain, r, pp);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            sr += r[j];
+            sp += pp[j];
+        }
+    }
+    for (int64_t i = lo + whole + threadIdx.x; i < hi; i += kThreads) {
         const Weights w = weights(p, q, i, certain);
         sr += w.r;
         sp += w.p;
@@ -145,14 +186,18 @@ __device__ double scan(double x, double* s_wave, double& all) {
     return before + x;
 }
 
+// sixteen consecutive entries per thread are weighed in registers, kept across the scan
 template <typename T>
 __global__ __launch_bounds__(kThreads) void draw_kernel(const AcceptArgs A) {
+    constexpr int N = Packed<T>::N, PER = 16;
     __shared__ double s_wave[4];
     __shared__ double s_before;
-    __shared__ int s_piece, s_pos, s_last;
+    __shared__ int s_piece, s_last;
     __shared__ long long s_at, s_end;
     const int n = blockIdx.x, t = threadIdx.x;
-    const Row R = find_row<T>(A, n);
+    Row R;
+    R.kept = A.accepted[n];  // the first launch's
+    R.rejected = R.kept < (A.num_drafts ? min(max(A.num_drafts[n], 0), A.num_draft) : A.num_draft);
     const T *p, *q;
     int64_t certain;
     row_of(A, n, R, p, q, certain);
@@ -163,52 +208,73 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(const AcceptArgs A) {
         s_end = -1;
     }
     // the piece that holds the draw: the first whose inclusive sum exceeds u * total
-    double mine = t < A.pieces ? A.partial[2 * ((int64_t)n * A.pieces + t)] : 0.0, all;
+    const double mine_r = t < A.pieces ? A.partial[2 * ((int64_t)n * A.pieces + t)] : 0.0;
+    const double mine_p = t < A.pieces ? A.partial[2 * ((int64_t)n * A.pieces + t) + 1] : 0.0;
+    const double u = (double)A.uniforms[(int64_t)n * (A.num_draft + 1) + A.num_draft];
+    double mine = mine_r, all;
     double inc = scan(mine, s_wave, all);
     const bool plain = !(all > 0.0);  // nothing left: draw from p
     if (plain) {
-        mine = t < A.pieces ? A.partial[2 * ((int64_t)n * A.pieces + t) + 1] : 0.0;
+        mine = mine_p;
         inc = scan(mine, s_wave, all);
     }
-    const double u = (double)A.uniforms[(int64_t)n * (A.num_draft + 1) + A.num_draft];
     const double target = u * all;
     if (mine > 0.0) {
         if (inc > target) atomicMin(&s_piece, t);
         atomicMax(&s_last, t);
     }
     __syncthreads();
-    const int piece = s_piece < A.pieces ? s_piece : s_last;  // u * total not below any sum: the last entry
-    if (t == piece) s_before = s_piece < A.pieces ? inc - mine : 0.0;
+    const bool inside = s_piece < A.pieces;
+    const int piece = inside ? s_piece : s_last;  // u * total not below any sum: the last entry
+    if (t == piece) s_before = inside ? inc - mine : 0.0;
     __syncthreads();
     int64_t drawn = -1;
     if (piece >= 0) {  // -1: no entry has any weight
         const int64_t lo = piece * A.piece, hi = min(lo + A.piece, A.vocab);
-        const int64_t per = (hi - lo + kThreads - 1) / kThreads;
-        const int64_t a = min(lo + t * per, hi), b = min(a + per, hi);
-        double sum = 0.0;
-        for (int64_t i = a; i < b; ++i) {
-            const Weights w = weights(p, q, i, certain);
-            sum += plain ? w.p : w.r;
-        }
-        double local_all;
-        double end = s_before + scan(sum, s_wave, local_all);
-        double c = end - sum;
-        int64_t first = A.vocab, last = -1;
-        for (int64_t i = a; i < b; ++i) {
-            const Weights w = weights(p, q, i, certain);
-            const double x = plain ? w.p : w.r;
-            c += x;
-            if (x > 0.0) {
-                if (c > target && first == A.vocab) first = i;
-                last = i;
+        double before = s_before;
+        for (int64_t at = lo; at < hi; at += PER * kThreads) {
+            const int64_t i0 = at + PER * t;
+            double w[PER], sum = 0.0;
+#pragma unroll
+            for (int k = 0; k < PER / N; ++k) {
+                const int64_t i = i0 + N * k;
+                double r[N] = {}, pp[N] = {};
+                if (i + N <= hi) {
+                    weights16(p, q, i, certain, r, pp);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (i + j < hi) {
+                            const Weights x = weights(p, q, i + j, certain);
+                            r[j] = x.r;
+                            pp[j] = x.p;
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    w[N * k + j] = plain ? pp[j] : r[j];
+                    sum += w[N * k + j];
+                }
             }
+            double local_all;
+            double c = before + scan(sum, s_wave, local_all) - sum;
+            int64_t first = A.vocab, last = -1;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                c += w[j];
+                if (w[j] > 0.0) {
+                    if (c > target && first == A.vocab) first = i0 + j;
+                    last = i0 + j;
+                }
+            }
+            if (first < A.vocab) atomicMin(&s_at, (long long)first);
+            if (last >= 0) atomicMax(&s_end, (long long)last);
+            before += local_all;
+            __syncthreads();
+            if (inside && s_at < A.vocab) break;
         }
-        if (first < A.vocab) atomicMin(&s_at, (long long)first);
-        if (last >= 0) atomicMax(&s_end, (long long)last);
-        __syncthreads();
-        drawn = (s_piece < A.pieces && s_at < A.vocab) ? s_at : s_end;
+        drawn = (inside && s_at < A.vocab) ? s_at : s_end;
     }
-    if (t == 0) A.accepted[n] = R.kept;
     for (int j = t; j <= A.num_draft; j += kThreads)
         A.out[(int64_t)n * (A.num_draft + 1) + j] =
             j < R.kept ? A.tokens[(int64_t)n * A.num_draft + j] : (j == R.kept ? (int32_t)drawn : -1);

@@ -13,29 +13,31 @@ from .ops import _DT, _check_cu_host, _check_out, _ptr
 
 
 def _tokens(name, t, heads, d, dtype, device):
-    """q, k or v flattened to tokens: the heads of a token are dense, the tokens a fixed
-    stride apart (a slice of a fused projection).  Returns the stride in elements."""
+    """q, k or v as rows of tokens: the heads of a token are dense, the tokens a fixed stride
+    apart (a slice of a fused projection).  Returns the stride in elements."""
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() < 3 or t.shape[-1] != d or t.shape[-2] != heads:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [..., {heads}, {d}]")
+    shape = t.shape
+    if len(shape) < 3 or shape[-1] != d or shape[-2] != heads:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [..., {heads}, {d}]")
     if t.is_contiguous():
         return heads * d
     st = t.stride()
     if st[-1] != 1 or (heads > 1 and st[-2] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous (strides {st})")
-    if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and st[0] != t.shape[1] * st[1]:
+    if len(shape) == 4 and shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
         raise ValueError(f"{name}: tokens must be a fixed stride apart (strides {st})")
-    step = st[0] if t.dim() == 4 and t.shape[1] == 1 else st[-3]
-    if t.numel() == 0 or t.shape[:-2].numel() == 1:
+    if t.numel() == 0 or shape[:-2].numel() == 1:
         return heads * d  # no second token to stride to
-    return step
+    return st[0] if len(shape) == 4 and shape[1] == 1 else st[-3]
 
 
-def _gates(name, t, shape, device):
-    _check_out(name, t, shape, torch.float32, device)
+def _dense(name, t, shape, dtype, device):
+    """A dense tensor of exactly this shape, dtype and device."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _check_out(name, t, shape, dtype, device)
 
 
 def _head_dims(q, v):
@@ -43,34 +45,38 @@ def _head_dims(q, v):
         raise ValueError("q must be a GPU tensor")
     if q.dtype not in _DT:
         raise ValueError(f"unsupported dtype {q.dtype}")
-    if q.dim() < 3 or v.dim() != q.dim():
+    qs, vs = q.shape, v.shape
+    if len(qs) < 3 or len(vs) != len(qs):
         raise ValueError("q and v must be [..., heads, d] with the same number of dimensions")
-    return q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1]
+    return qs[-2], vs[-2], qs[-1], vs[-1]
 
 
-def _params(q, k, v, lead, scale):
+def _params(q, k, v, scale):
     hk, hv, dk, dv = _head_dims(q, v)
-    if tuple(q.shape[:-2]) != lead or tuple(k.shape[:-2]) != lead or tuple(v.shape[:-2]) != lead:
-        raise ValueError(f"q, k and v must lead with {lead}: {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
-    s = [_tokens(n, t, h, d, q.dtype, q.device) for n, t, h, d in (("q", q, hk, dk), ("k", k, hk, dk), ("v", v, hv, dv))]
-    return _lib.GdnParams(_DT[q.dtype], hk, hv, dk, dv, float(scale), *s)
+    lead = q.shape[:-2]
+    if k.shape[:-2] != lead or v.shape[:-2] != lead:
+        raise ValueError(f"q, k and v must lead with {tuple(lead)}: {tuple(k.shape)}, {tuple(v.shape)}")
+    dt, dev = q.dtype, q.device
+    return _lib.GdnParams(_DT[dt], hk, hv, dk, dv, scale, _tokens("q", q, hk, dk, dt, dev),
+                          _tokens("k", k, hk, dk, dt, dev), _tokens("v", v, hv, dv, dt, dev))
 
 
 class _on:
     """The call runs on the inputs' device and on that device's current stream."""
 
+    __slots__ = ("device", "guard")
+
     def __init__(self, device):
-        self.device = device
-        self.other = device.index is not None and device.index != torch.cuda.current_device()
+        self.device, self.guard = device, None
 
     def __enter__(self):
-        if self.other:
+        if self.device.index != torch.cuda.current_device():
             self.guard = torch.cuda.device(self.device)
             self.guard.__enter__()
         return torch.cuda.current_stream(self.device).cuda_stream
 
     def __exit__(self, *exc):
-        if self.other:
+        if self.guard is not None:
             self.guard.__exit__(*exc)
 
 
@@ -106,19 +112,19 @@ def gdn_chunk_prefill(q, k, v, log_alpha, beta, cu_seqlens: Optional[Sequence[in
     tensor.  Returns (o, final_state or None); o has v's shape and dtype."""
     cu, T = _lengths(q, cu_seqlens)
     N, dev = len(cu) - 1, q.device
-    p = _params(q, k, v, tuple(q.shape[:-2]), scale)
+    p = _params(q, k, v, scale)
     hv, dk, dv = p.num_v_heads, p.dk, p.dv
-    gshape = tuple(q.shape[:-2]) + (hv,)
-    _gates("log_alpha", log_alpha, gshape, dev)
-    _gates("beta", beta, gshape, dev)
+    gshape = v.shape[:-1]
+    _dense("log_alpha", log_alpha, gshape, torch.float32, dev)
+    _dense("beta", beta, gshape, torch.float32, dev)
     if initial_state is not None:
-        _check_out("initial_state", initial_state, (N, hv, dk, dv), torch.float32, dev)
+        _dense("initial_state", initial_state, (N, hv, dk, dv), torch.float32, dev)
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
     else:
-        _check_out("out", out, v.shape, v.dtype, dev)
+        _dense("out", out, v.shape, v.dtype, dev)
     if final_state is not None:
-        _check_out("final_state", final_state, (N, hv, dk, dv), torch.float32, dev)
+        _dense("final_state", final_state, (N, hv, dk, dv), torch.float32, dev)
     elif output_final_state:
         final_state = torch.empty((N, hv, dk, dv), dtype=torch.float32, device=dev)
     lib = _lib.load()
@@ -141,15 +147,15 @@ def gdn_prefill_backward(q, k, v, log_alpha, beta, d_out,
     allocate one."""
     cu, T = _lengths(q, cu_seqlens)
     N, dev = len(cu) - 1, q.device
-    p = _params(q, k, v, tuple(q.shape[:-2]), scale)
+    p = _params(q, k, v, scale)
     hv, dk, dv = p.num_v_heads, p.dk, p.dv
-    gshape = tuple(q.shape[:-2]) + (hv,)
-    _gates("log_alpha", log_alpha, gshape, dev)
-    _gates("beta", beta, gshape, dev)
-    _check_out("d_out", d_out, v.shape, v.dtype, dev)
+    gshape = v.shape[:-1]
+    _dense("log_alpha", log_alpha, gshape, torch.float32, dev)
+    _dense("beta", beta, gshape, torch.float32, dev)
+    _dense("d_out", d_out, v.shape, v.dtype, dev)
     for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state)):
         if t is not None:
-            _check_out(name, t, (N, hv, dk, dv), torch.float32, dev)
+            _dense(name, t, (N, hv, dk, dv), torch.float32, dev)
     new = lambda like, dtype: torch.empty(like.shape, dtype=dtype, device=dev)  # noqa: E731
     g = dict(dq=new(q, q.dtype), dk=new(k, k.dtype), dv=new(v, v.dtype), dlog_alpha=new(log_alpha, torch.float32),
              dbeta=new(beta, torch.float32),
@@ -162,7 +168,7 @@ def gdn_prefill_backward(q, k, v, log_alpha, beta, d_out,
                 raise _lib.KdaError(_lib.KDA_ERR_INVALID_ARGUMENT, lib.kda_last_error().decode())
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
         else:
-            _check_out("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+            _dense("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
         _lib.check(lib.kda_gdn_prefill_backward(
             ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), cu_h, N,
             _ptr(initial_state), _ptr(d_out), _ptr(d_final_state), _ptr(g["dq"]), _ptr(g["dk"]),
@@ -192,24 +198,24 @@ def gdn_recurrent(q, k, v, log_alpha, beta, state, steps: Optional[torch.Tensor]
     else:
         raise ValueError("q must be [N, K, HK, dk] or [N, HK, dk]")
     dev = q.device
-    p = _params(q, k, v, tuple(q.shape[:-2]), scale)
-    gshape = tuple(q.shape[:-2]) + (hv,)
-    _gates("log_alpha", log_alpha, gshape, dev)
-    _gates("beta", beta, gshape, dev)
+    p = _params(q, k, v, scale)
+    gshape = v.shape[:-1]
+    _dense("log_alpha", log_alpha, gshape, torch.float32, dev)
+    _dense("beta", beta, gshape, torch.float32, dev)
     if state.dim() != 4:
         raise ValueError(f"state has shape {tuple(state.shape)}, expected [slots, {hv}, {dk}, {dv}]")
     slots = state.shape[0]
-    _check_out("state", state, (slots, hv, dk, dv), torch.float32, dev)
+    _dense("state", state, (slots, hv, dk, dv), torch.float32, dev)
     for name, t in (("steps", steps), ("state_indices", state_indices)):
         if t is not None:
-            _check_out(name, t, (N,), torch.int32, dev)
+            _dense(name, t, (N,), torch.int32, dev)
     if not output:
         if out is not None:
             raise ValueError("out given but output=False")
     elif out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
     else:
-        _check_out("out", out, v.shape, v.dtype, dev)
+        _dense("out", out, v.shape, v.dtype, dev)
     if N == 0:
         return out
     lib = _lib.load()
@@ -236,23 +242,23 @@ def spec_accept(target_probs, draft_probs, draft_tokens, uniforms,
     if target_probs.dim() != 3 or target_probs.dtype not in _DT or target_probs.shape[1] < 1 or target_probs.shape[2] < 1:
         raise ValueError(f"target_probs must be bf16 or fp32 [N, K+1, V], got {tuple(target_probs.shape)} {target_probs.dtype}")
     N, K, V, dev = target_probs.shape[0], target_probs.shape[1] - 1, target_probs.shape[2], target_probs.device
-    _check_out("target_probs", target_probs, (N, K + 1, V), target_probs.dtype, dev)
+    _dense("target_probs", target_probs, (N, K + 1, V), target_probs.dtype, dev)
     if draft_probs is not None:
-        _check_out("draft_probs", draft_probs, (N, K, V), target_probs.dtype, dev)
+        _dense("draft_probs", draft_probs, (N, K, V), target_probs.dtype, dev)
         if K == 0:
             draft_probs = None
-    _check_out("draft_tokens", draft_tokens, (N, K), torch.int32, dev)
-    _check_out("uniforms", uniforms, (N, K + 1), torch.float32, dev)
+    _dense("draft_tokens", draft_tokens, (N, K), torch.int32, dev)
+    _dense("uniforms", uniforms, (N, K + 1), torch.float32, dev)
     if num_drafts is not None:
-        _check_out("num_drafts", num_drafts, (N,), torch.int32, dev)
+        _dense("num_drafts", num_drafts, (N,), torch.int32, dev)
     if accepted is None:
         accepted = torch.empty((N,), dtype=torch.int32, device=dev)
     else:
-        _check_out("accepted", accepted, (N,), torch.int32, dev)
+        _dense("accepted", accepted, (N,), torch.int32, dev)
     if tokens is None:
         tokens = torch.empty((N, K + 1), dtype=torch.int32, device=dev)
     else:
-        _check_out("tokens", tokens, (N, K + 1), torch.int32, dev)
+        _dense("tokens", tokens, (N, K + 1), torch.int32, dev)
     if N == 0:
         return accepted, tokens
     lib = _lib.load()
