@@ -117,7 +117,7 @@ __device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t ro
     constexpr int STEP = L::ROWG * DV;
 #pragma unroll
     for (int i = 0; i < L::RPT; ++i)
-        s[i] = Sin ? *reinterpret_cast<const f32x4*>(Sin + at + i * STEP) : zero4();
+        s[i] = Sin ? __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(Sin + at + i * STEP)) : zero4();
     Stage<T, DK, DV, NV, TB> st;
     st.load(A, row0, min(n, TB), hk, head, col0);
     bool twice = false;  // an earlier row of this call names the same slot
@@ -237,9 +237,17 @@ __global__ __launch_bounds__(kThreads, TB <= 4 ? 4 : 3) void step_kernel(const R
 // One token per sequence, the decode step: the same arithmetic in the same order as walk's, with
 // nothing in registers but the state and what a row needs.  The token's loads are issued before
 // the state's and the barriers order LDS alone, so k, q and the repeated-slot check are done
-// while the state is on its way.
+// while the state is on its way.  Whole rows: the state is streamed past the caches both ways,
+// and no more than 128 KiB of states are in work on a compute unit (unused LDS keeps further
+// workgroups out): with more reading and writing at once memory pages change more often.
+// 256 x 32 states of 128 x 128 in a pool, slots in random order: 220 us, 195 with streamed
+// loads, 193 with three workgroups per unit, 181 with two (5.9 TB/s; a large copy reaches 4.8
+// on the same card).
+template <int DK, int DV>
+constexpr int whole_lds() { return DK * DV * 4 / 8 * 7; }
+
 template <typename T, int DK, int DV, int NV>
-__global__ __launch_bounds__(kThreads, 4) void decode_kernel(const RecArgs A) {
+__global__ __launch_bounds__(kThreads, DK * NV == 128 * 128 ? 2 : 4) void decode_kernel(const RecArgs A) {
     using L = Tile<DK, NV, 1>;
     constexpr int SL = DV / NV, STEP = L::ROWG * DV;
     __shared__ __attribute__((aligned(16))) float s_k[DK], s_q[DK];
@@ -270,7 +278,7 @@ __global__ __launch_bounds__(kThreads, 4) void decode_kernel(const RecArgs A) {
     __builtin_amdgcn_sched_barrier(0);
     f32x4 s[L::RPT];
 #pragma unroll
-    for (int i = 0; i < L::RPT; ++i) s[i] = *reinterpret_cast<const f32x4*>(S + i * STEP);
+    for (int i = 0; i < L::RPT; ++i) s[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(S + i * STEP));
     __builtin_amdgcn_sched_barrier(0);
     if (t < DK) {
         s_k[t] = kv;
@@ -371,7 +379,7 @@ hipError_t launch_gdn_recurrent(const GdnRecurrentArgs& a, hipStream_t stream) {
         using T = decltype(t);
         constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value, NV = decltype(nv)::value;
         if (a.num_tokens == 1 && a.nv == DV)  // whole rows
-            hipLaunchKernelGGL((decode_kernel<T, DK, DV, DV>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, r);
+            hipLaunchKernelGGL((decode_kernel<T, DK, DV, DV>), dim3((unsigned)blocks), dim3(kThreads), (whole_lds<DK, DV>()), stream, r);
         else if (a.num_tokens == 1)
             hipLaunchKernelGGL((decode_kernel<T, DK, DV, NV>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, r);
         else if (a.num_tokens <= 4)
