@@ -456,6 +456,7 @@ __global__ __launch_bounds__(256, 2) void gdn_gradients_kernel(const GdnBackward
     // ---------------------------------------------------------------- over the value columns
     struct Slice {
         u32x4 s[2][C::PS], d[2][C::PS], u[2], x[2], o[1];
+        u32x2 v[2];  // V of token tile `wave`: lane (r, g) has token r, columns 4g .. and 16 + 4g ..
     } y;
     auto load = [&](int n) {
         const int64_t at = (int64_t)32 * n;
@@ -470,6 +471,9 @@ __global__ __launch_bounds__(256, 2) void gdn_gradients_kernel(const GdnBackward
             y.x[pl] = *reinterpret_cast<const u32x4*>(px + pl * (int64_t)kGC * DV + at * kGC + 8 * tid);
         }
         load_rows<1, 4>(y.o, po + at, os, rows, tid);
+        const __amdgpu_buffer_rsrc_t rv = rsrc(pv + at, ((rows - 1) * (int)d.vs + 32) * 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) y.v[i] = bload8(rv, (uint32_t)((16 * wave + r) * (int)d.vs + 16 * i + 4 * g) * 2);
     };
     auto put = [&]() {
 #pragma unroll
@@ -524,79 +528,96 @@ __global__ __launch_bounds__(256, 2) void gdn_gradients_kernel(const GdnBackward
     for (int b = 0; b < C::KW / 2; ++b) tr[b] = zero4();
     float xv = 0.f;
     load(0);
+#pragma unroll 1
     for (int n = 0; n < DV / 32; ++n) {
-        __syncthreads();
+        lds_barrier();
         put();
-        __syncthreads();
+        const u32x2 vcur[2] = {y.v[0], y.v[1]};
+        lds_barrier();
         if (n + 1 < DV / 32) load(n + 1);
-        bf16x8 o[2], xh[2], xl[2], uh[2], ul[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int t = 2 * wi + x;
-            o[x] = outs(t);
-            xh[x] = tokens(C::XH, t);
-            xl[x] = tokens(C::XL, t);
-            uh[x] = tokens(C::UH, t);
-            ul[x] = tokens(C::UL, t);
-        }
-#pragma unroll
-        for (int b = 0; b < C::KW; ++b) {
-            const bf16x8 sh = channels(C::SH, C::KW * wj + b), sl = channels(C::SL, C::KW * wj + b);
+        // (the scheduling barriers keep operands from being read further ahead than fits the
+        // registers)
+        bf16x8 xh[2], xl[2];
+        {
+            bf16x8 o[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                OS[x][b] = mfma32(sh, o[x], OS[x][b]);
-                XS[x][b] = mfma32(sh, xh[x], XS[x][b]);
-                OS[x][b] = mfma32(sl, o[x], OS[x][b]);
-                XS[x][b] = mfma32(sl, xh[x], XS[x][b]);
-                XS[x][b] = mfma32(sh, xl[x], XS[x][b]);
+                o[x] = outs(2 * wi + x);
+                xh[x] = tokens(C::XH, 2 * wi + x);
+                xl[x] = tokens(C::XL, 2 * wi + x);
             }
-            const bf16x8 dh = channels(C::DH, C::KW * wj + b), dl = channels(C::DL, C::KW * wj + b);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                UD[x][b] = mfma32(dh, uh[x], UD[x][b]);
-                UD[x][b] = mfma32(dl, uh[x], UD[x][b]);
-                UD[x][b] = mfma32(dh, ul[x], UD[x][b]);
+            for (int b = 0; b < C::KW; ++b) {
+                const bf16x8 sh = channels(C::SH, C::KW * wj + b), sl = channels(C::SL, C::KW * wj + b);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    OS[x][b] = mfma32(sh, o[x], OS[x][b]);
+                    XS[x][b] = mfma32(sh, xh[x], XS[x][b]);
+                    OS[x][b] = mfma32(sl, o[x], OS[x][b]);
+                    XS[x][b] = mfma32(sl, xh[x], XS[x][b]);
+                    XS[x][b] = mfma32(sh, xl[x], XS[x][b]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            // the diagonal of S dS'^T, every channel tile by one of the two waves that hold it
-            if (b / (C::KW / 2) == wi) {
-                f32x4& z = tr[b % (C::KW / 2)];
-                z = mfma32(sh, dh, z);
-                z = mfma32(sl, dh, z);
-                z = mfma32(sh, dl, z);
-            }
-        }
-        for (int m = 0; m < ntile; ++m) {
-            int it, jt;
-            tile(m, it, jt);
-            const bf16x8 u1 = tokens(C::UH, jt), u2 = tokens(C::UL, jt), oi = outs(it), x1 = tokens(C::XH, it), x2 = tokens(C::XL, it);
-            f32x4 ou = OU[0], xu = XU[0];
-            if (m == 1) { ou = OU[1]; xu = XU[1]; }
-            if (m == 2) { ou = OU[2]; xu = XU[2]; }
-            ou = mfma32(u1, oi, ou);
-            xu = mfma32(u1, x1, xu);
-            ou = mfma32(u2, oi, ou);
-            xu = mfma32(u2, x1, xu);
-            xu = mfma32(u1, x2, xu);
-            if (m == 0) { OU[0] = ou; XU[0] = xu; }
-            if (m == 1) { OU[1] = ou; XU[1] = xu; }
-            if (m == 2) { OU[2] = ou; XU[2] = xu; }
         }
         // dV = beta dX and dX . V of token tile `wave`: lane (r, g) has token r, eight columns
         {
             const bf16x8 x1 = wj ? xh[1] : xh[0], x2 = wj ? xl[1] : xl[0];
             const f32x4 a0 = lower(x1) + lower(x2), a1 = upper(x1) + upper(x2);
             const int tok = 16 * wave + r;
+            const f32x4 v0 = unpack_bf4(vcur[0]), v1 = unpack_bf4(vcur[1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xv += a0[i] * v0[i] + a1[i] * v1[i];
             if (tok < rows) {
                 const float be = lds_ld<float>(smem + C::GV + GateVec::BE + 4 * tok);
-                const bf16* vr = pv + tok * d.vs + 32 * n + 4 * g;
-                const f32x4 v0 = to_f4(*reinterpret_cast<const bf16x4*>(vr)), v1 = to_f4(*reinterpret_cast<const bf16x4*>(vr + 16));
                 bf16* dst = (bf16*)A.dv + (t0 + tok) * os + (int64_t)h * DV + 32 * n + 4 * g;
                 *reinterpret_cast<bf16x4*>(dst) = to_bf4(be * a0);
                 *reinterpret_cast<bf16x4*>(dst + 16) = to_bf4(be * a1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) xv += a0[i] * v0[i] + a1[i] * v1[i];
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        {
+            bf16x8 uh[2], ul[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uh[x] = tokens(C::UH, 2 * wi + x);
+                ul[x] = tokens(C::UL, 2 * wi + x);
+            }
+#pragma unroll
+            for (int b = 0; b < C::KW; ++b) {
+                const bf16x8 dh = channels(C::DH, C::KW * wj + b), dl = channels(C::DL, C::KW * wj + b);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    UD[x][b] = mfma32(dh, uh[x], UD[x][b]);
+                    UD[x][b] = mfma32(dl, uh[x], UD[x][b]);
+                    UD[x][b] = mfma32(dh, ul[x], UD[x][b]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        // the diagonal of S dS'^T, every channel tile by one of the two waves that hold it
+#pragma unroll
+        for (int b = 0; b < C::KW / 2; ++b) {
+            const int ch = C::KW * wj + C::KW / 2 * wi + b;
+            const bf16x8 sh = channels(C::SH, ch), dh = channels(C::DH, ch);
+            tr[b] = mfma32(sh, dh, tr[b]);
+            tr[b] = mfma32(channels(C::SL, ch), dh, tr[b]);
+            tr[b] = mfma32(sh, channels(C::DL, ch), tr[b]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        unroll<0, 3>([&](auto M) {
+            constexpr int m = decltype(M)::value;
+            if (m >= ntile) return;
+            int it, jt;
+            tile(m, it, jt);
+            const bf16x8 u1 = tokens(C::UH, jt), u2 = tokens(C::UL, jt), oi = outs(it), x1 = tokens(C::XH, it), x2 = tokens(C::XL, it);
+            OU[m] = mfma32(u1, oi, OU[m]);
+            XU[m] = mfma32(u1, x1, XU[m]);
+            OU[m] = mfma32(u2, oi, OU[m]);
+            XU[m] = mfma32(u2, x1, XU[m]);
+            XU[m] = mfma32(u1, x2, XU[m]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
     }
     // ---------------------------------------------------------------- over the chunk's tokens
     u32x4 rk[KeyTile<DK>::PPT], rq[KeyTile<DK>::PPT];
@@ -722,6 +743,7 @@ __global__ __launch_bounds__(256, 2) void gdn_gradients_kernel(const GdnBackward
                     dk[b] = mfma32(kc, fh, dk[b]);
                     dq[b] = mfma32(kc, el, dq[b]);
                     dk[b] = mfma32(kc, fl, dk[b]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
             if (s >= wi) {  // rows of half s: E^T Q, F^T K
@@ -733,6 +755,7 @@ __global__ __launch_bounds__(256, 2) void gdn_gradients_kernel(const GdnBackward
                     dk[b] = mfma32(kc, fh, dk[b]);
                     dk[b] = mfma32(qc, el, dk[b]);
                     dk[b] = mfma32(kc, fl, dk[b]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
