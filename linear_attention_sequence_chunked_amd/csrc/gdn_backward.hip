@@ -95,23 +95,32 @@ __global__ __launch_bounds__((WCfg<DK, NCB>::THREADS)) void gdn_walk_back_kernel
     auto chunk = [&](int c) { return nch - 1 - c; };
 
     using std::integral_constant;
+    constexpr int R = 3;  // chunks of loads in flight, and the passes' rounds, as in the prefill
+    const int passes = (nch + R) / R * R;
+    auto drain = [&]() {
+        for (int c = nch + 1; c < passes; ++c) {
+            lds_barrier();
+            lds_barrier();
+        }
+    };
     if (wave >= C::W_STAGE && wave < C::W_INV) {
         struct Staged {
             u32x4 k[C::K::PPT], q[C::K::PPT], o[C::V::PPT];
             float la, be;
-        } x[2];
+        };
+        Staged x[R];
         const int st = tid - 64 * C::W_STAGE;
         auto load = [&](Staged& y, int c) {
-            const int rows = min(kGC, len - kGC * chunk(c));
-            const int64_t at = start + (int64_t)kGC * chunk(c);
+            // (chunks before the first are loaded over an empty range: no branch between a load and
+            // its use)
+            const int rows = c < nch ? min(kGC, len - kGC * chunk(c)) : 0;
+            const int64_t at = start + (int64_t)kGC * max(chunk(c), 0);
+            const int gates = wave == C::W_STAGE && rows > 0 ? ((rows - 1) * a.hv + 1) * 4 : 0;
             load_rows<C::K::PPT, DK / 8>(y.k, a.k + at * a.ks + (int64_t)hk * DK, a.ks, rows, st);
             load_rows<C::K::PPT, DK / 8>(y.q, a.q + at * a.qs + (int64_t)hk * DK, a.qs, rows, st);
             load_rows<C::V::PPT, C::NV / 8>(y.o, a.d_out + at * os + (int64_t)h * a.dv + col0, os, rows, st);
-            y.la = y.be = 0.f;
-            if (wave == C::W_STAGE && lane < rows) {
-                y.la = a.la[(at + lane) * a.hv + h];
-                y.be = a.be[(at + lane) * a.hv + h];
-            }
+            y.la = bload4f(rsrc(a.la + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
+            y.be = bload4f(rsrc(a.be + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
         };
         auto stage = [&](const Staged& y, int c) {
             unsigned char* Ot = buf(C::O_O, C::V::SIZE, c);
@@ -136,14 +145,16 @@ __global__ __launch_bounds__((WCfg<DK, NCB>::THREADS)) void gdn_walk_back_kernel
                 if (lane == 0) lds_st(vec + C::V_GC, __builtin_amdgcn_exp2f((float)GC));
             }
         };
-        if (nch > 0) load(x[0], 0);
-        if (nch > 1) load(x[1], 1);
-        for (int c = 0; c <= nch; c += 2) {
-            unroll<0, 2>([&](auto J) {
+        unroll<0, R>([&](auto J) {
+            load(x[decltype(J)::value], decltype(J)::value);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        for (int c = 0; c < passes; c += R) {
+            unroll<0, R>([&](auto J) {
                 constexpr int j = decltype(J)::value;
-                if (c + j > nch) return;
-                if (c + j < nch) stage(x[j], c + j);
-                if (c + j + 2 < nch) load(x[j], c + j + 2);
+                stage(x[j], c + j);
+                load(x[j], c + j + R);
+                __builtin_amdgcn_sched_barrier(0);
                 lds_barrier();
                 lds_barrier();
             });
@@ -172,6 +183,7 @@ __global__ __launch_bounds__((WCfg<DK, NCB>::THREADS)) void gdn_walk_back_kernel
             if (c < nch) x = half_columns<DK, false>(buf(C::O_K, C::K::SIZE, c), buf(C::O_G, GateVec::SIZE, c), sc, n, lane);
             lds_barrier();
         }
+        drain();
         return;
     }
     if (wave >= C::W_GRAM) {
@@ -230,6 +242,7 @@ __global__ __launch_bounds__((WCfg<DK, NCB>::THREADS)) void gdn_walk_back_kernel
             }
             lds_barrier();
         }
+        drain();
         return;
     }
 
@@ -382,6 +395,7 @@ __global__ __launch_bounds__((WCfg<DK, NCB>::THREADS)) void gdn_walk_back_kernel
         if (c + 1 < nch) load_k(kf[0], c + 1, 0);
         lds_barrier();
     }
+    drain();
     if (a.dS0) {
 #pragma unroll
         for (int b = 0; b < KB; ++b)

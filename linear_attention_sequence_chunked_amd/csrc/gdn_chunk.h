@@ -68,6 +68,10 @@ __device__ __forceinline__ void load_rows(u32x4 (&dst)[PPT], const bf16* base, i
     }
 }
 
+__device__ __forceinline__ float bload4f(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
+}
+
 // [64][DK] rows to LDS
 template <int DK, bool HALF>
 __device__ __forceinline__ void store_key(unsigned char* tile, const u32x4 (&src)[KeyTile<DK>::PPT], int tid) {

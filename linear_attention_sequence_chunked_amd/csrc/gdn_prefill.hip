@@ -134,28 +134,39 @@ __global__ __launch_bounds__((GCfg<DK, NCB, SAVE>::THREADS)) void gdn_prefill_ke
     const int os = a.hv * a.dv;  // output stride (the host bounds 64 rows of it to 32 bits)
 
     using std::integral_constant;
+    // the narrow form's passes come in rounds of the staging ring; those behind the last chunk's
+    // only keep the barriers
+    constexpr int R = C::NARROW ? 3 : 1;
+    const int passes = (nch + R) / R * R;
+    auto drain = [&]() {
+        for (int c = nch + 1; c < passes; ++c) {
+            lds_barrier();
+            lds_barrier();
+        }
+    };
     // ------------------------------------------------------------------ parts of the key side
     struct Staged {
         u32x4 k[C::K::PPT], q[C::K::PPT], v[C::V::PPT];
         float la, be;
     };
     const int st = tid - 64 * C::W_STAGE;  // thread among the staging waves
+    // No branch may lie between a load and its use: the compiler would wait for every load in
+    // flight there.  So chunks behind the last, and the gates in all waves but one, are loaded over
+    // an empty range (nothing is read, the registers get zeros).
     auto load = [&](Staged& x, int c) {
         const int rows = min(kGC, len - kGC * c);
         const int64_t at = start + (int64_t)kGC * c;
+        const int gates = wave == C::W_STAGE && rows > 0 ? ((rows - 1) * a.hv + 1) * 4 : 0;
         load_rows<C::K::PPT, DK / 8>(x.k, a.k + at * a.ks + (int64_t)hk * DK, a.ks, rows, st);
         if constexpr (C::OUT) load_rows<C::K::PPT, DK / 8>(x.q, a.q + at * a.qs + (int64_t)hk * DK, a.qs, rows, st);
         load_rows<C::V::PPT, C::NV / 8>(x.v, a.v + at * a.vs + (int64_t)h * a.dv + col0, a.vs, rows, st);
-        x.la = x.be = 0.f;
-        if (wave == C::W_STAGE && lane < rows) {
-            x.la = a.la[(at + lane) * a.hv + h];
-            x.be = a.be[(at + lane) * a.hv + h];
-        }
+        x.la = bload4f(rsrc(a.la + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
+        x.be = bload4f(rsrc(a.be + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
     };
-    auto stage = [&](const Staged& x, int c, auto CONVERT) {  // CONVERT: the rows are bf16 still
+    auto stage = [&](const Staged& x, int c) {
         unsigned char* Vt = buf(C::O_V, C::V::SIZE, c);
-        store_key<DK, decltype(CONVERT)::value>(buf(C::O_K, C::K::SIZE, c), x.k, st);
-        if constexpr (C::OUT) store_key<DK, decltype(CONVERT)::value>(buf(C::O_Q, C::K::SIZE, c), x.q, st);
+        store_key<DK, true>(buf(C::O_K, C::K::SIZE, c), x.k, st);
+        if constexpr (C::OUT) store_key<DK, true>(buf(C::O_Q, C::K::SIZE, c), x.q, st);
 #pragma unroll
         for (int i = 0; i < C::V::PPT; ++i) {
             const int e = st + 256 * i;
@@ -194,29 +205,26 @@ __global__ __launch_bounds__((GCfg<DK, NCB, SAVE>::THREADS)) void gdn_prefill_ke
         }
     };
     // P's tiles (it, J0 .. J1-1), and -A's where they lie below the halves: lane (r, g) holds
-    // row 16 it + r, columns 16 jt + 4g ..
-    auto gram_row = [&](auto IT, auto J0, auto J1, int c) {
+    // row 16 it + r, columns 16 jt + 4g ..  A gram wave keeps the rows of K it needs.
+    typedef TileRows<DK> KeyRows[4];
+    auto gram_row = [&](const KeyRows& k, auto IT, auto J0, auto J1, int c) {
         constexpr int it = decltype(IT)::value;
-        const unsigned char* Kt = buf(C::O_K, C::K::SIZE, c);
         const unsigned char* gv = buf(C::O_G, GateVec::SIZE, c);
         unsigned char* M = buf(C::O_M, C::M_SIZE, c);
-        TileRows<DK> qt, ki;
+        TileRows<DK> qt;
         if constexpr (C::OUT) qt.load(buf(C::O_Q, C::K::SIZE, c), it, r, g);
-        if constexpr (it >= 2 && decltype(J0)::value < 2) ki.load(Kt, it, r, g);
         unroll<decltype(J0)::value, decltype(J1)::value>([&](auto JT) {
             constexpr int jt = decltype(JT)::value;
-            TileRows<DK> kj;
-            kj.load(Kt, jt, r, g);
             const f32x4 d = decay_row(gv, 16 * it + r, 16 * jt + 4 * g);
             if constexpr (C::OUT) {
-                f32x4 p = tile_dot(kj, qt);
+                f32x4 p = tile_dot(k[jt], qt);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) p[i] = it > jt || 4 * g + i <= r ? d[i] * p[i] : 0.f;
                 // P: block (rows 32 (it / 2), columns 32 (jt / 2)), row tile it % 2
                 lds_st(M + C::M_P + (2 * (it / 2 + jt / 2) + it % 2) * C::FR + 16 * lane + 8 * (jt % 2), to_h4(p));
             }
             if constexpr (it / 2 != jt / 2) {
-                const f32x4 x = tile_dot(kj, ki);
+                const f32x4 x = tile_dot(k[jt], k[it]);
                 const float nb = -lds_ld<float>(gv + GateVec::BE + 4 * (16 * it + r));
                 f16x4 hi, lo;
                 split4h(nb * (d * x), hi, lo, m1);
@@ -233,29 +241,34 @@ __global__ __launch_bounds__((GCfg<DK, NCB, SAVE>::THREADS)) void gdn_prefill_ke
     constexpr integral_constant<int, 4> i4;
     // one chunk's Gram work of gram wave n: the block of A below the halves with P's tiles
     // there, then P's other tiles (needed a phase later)
-    auto gram_first = [&](int n, int c) {
-        if (n == 0) gram_row(i2, i0, i2, c);
-        else gram_row(i3, i0, i2, c);
+    auto gram_first = [&](KeyRows& k, auto N, int c) {
+        constexpr int it = 2 + decltype(N)::value;
+        const unsigned char* Kt = buf(C::O_K, C::K::SIZE, c);
+        k[it].load(Kt, it, r, g);
+        k[0].load(Kt, 0, r, g);
+        k[1].load(Kt, 1, r, g);
+        if constexpr (it == 3 && C::OUT) k[2].load(Kt, 2, r, g);
+        gram_row(k, integral_constant<int, it>{}, i0, i2, c);
     };
-    auto gram_second = [&](int n, int c) {
+    auto gram_second = [&](const KeyRows& k, auto N, int c) {
         if constexpr (!C::OUT) return;
-        if (n == 0) {
-            gram_row(i2, i2, i3, c);
-            gram_row(i1, i0, i2, c);
+        if constexpr (decltype(N)::value == 0) {
+            gram_row(k, i2, i2, i3, c);
+            gram_row(k, i1, i0, i2, c);
         } else {
-            gram_row(i3, i2, i4, c);
-            gram_row(i0, i0, i1, c);
+            gram_row(k, i3, i2, i4, c);
+            gram_row(k, i0, i0, i1, c);
         }
     };
 
     if (!C::NARROW && wave >= C::W_STAGE) {
         // ---------------------------------------------------------------- wide: producers
         Staged x;
-        if (nch > 0) load(x, 0);
+        load(x, 0);
         for (int c = 0; c <= nch; ++c) {
             if (c < nch) {
-                stage(x, c, integral_constant<bool, true>{});
-                if (c + 1 < nch) load(x, c + 1);
+                stage(x, c);
+                load(x, c + 1);
             }
             lds_barrier();
             if (c < nch) {
@@ -263,8 +276,14 @@ __global__ __launch_bounds__((GCfg<DK, NCB, SAVE>::THREADS)) void gdn_prefill_ke
                     HalfState x = columns(c);
                     join(x, c);
                 } else {
-                    gram_first(wave - C::W_GRAM, c);
-                    gram_second(wave - C::W_GRAM, c);
+                    KeyRows k;
+                    if (wave == C::W_GRAM) {
+                        gram_first(k, i0, c);
+                        gram_second(k, i0, c);
+                    } else {
+                        gram_first(k, i1, c);
+                        gram_second(k, i1, c);
+                    }
                 }
             }
             lds_barrier();
@@ -272,27 +291,20 @@ __global__ __launch_bounds__((GCfg<DK, NCB, SAVE>::THREADS)) void gdn_prefill_ke
         return;
     }
     if (C::NARROW && wave >= C::W_STAGE && wave < C::W_INV) {
-        // two chunks of loads in flight; rows are converted in phase B, so that phase A only
-        // writes them
-        Staged x[2];
-        auto convert = [&](Staged& y) {
-#pragma unroll
-            for (int i = 0; i < C::K::PPT; ++i) {
-                y.k[i] = staged8<true>(y.k[i]);
-                if constexpr (C::OUT) y.q[i] = staged8<true>(y.q[i]);
-            }
-        };
-        if (nch > 0) load(x[0], 0);
-        if (nch > 1) load(x[1], 1);
-        convert(x[0]);
-        for (int c = 0; c <= nch; c += 2) {
-            unroll<0, 2>([&](auto J) {
+        // Three chunks of loads in flight.  (Chunks behind the last are staged too: nothing reads
+        // them.)
+        Staged x[R];
+        unroll<0, R>([&](auto J) {
+            load(x[decltype(J)::value], decltype(J)::value);
+            __builtin_amdgcn_sched_barrier(0);  // in this order
+        });
+        for (int c = 0; c < passes; c += R) {
+            unroll<0, R>([&](auto J) {
                 constexpr int j = decltype(J)::value;
-                if (c + j > nch) return;
-                if (c + j < nch) stage(x[j], c + j, integral_constant<bool, false>{});
-                if (c + j + 2 < nch) load(x[j], c + j + 2);
+                stage(x[j], c + j);
+                load(x[j], c + j + R);
+                __builtin_amdgcn_sched_barrier(0);
                 lds_barrier();
-                if (c + j + 1 < nch) convert(x[1 - j]);
                 lds_barrier();
             });
         }
@@ -306,15 +318,22 @@ __global__ __launch_bounds__((GCfg<DK, NCB, SAVE>::THREADS)) void gdn_prefill_ke
             if (c < nch) x = columns(c);
             lds_barrier();
         }
+        drain();
         return;
     }
     if (C::NARROW && wave >= C::W_GRAM && wave < C::W_OUT) {
-        for (int c = 0; c <= nch; ++c) {
-            if (c > 0) gram_second(wave - C::W_GRAM, c - 1);
-            lds_barrier();
-            if (c < nch) gram_first(wave - C::W_GRAM, c);
-            lds_barrier();
-        }
+        auto run = [&](auto N) {
+            KeyRows k;
+            for (int c = 0; c <= nch; ++c) {
+                if (c > 0) gram_second(k, N, c - 1);
+                lds_barrier();
+                if (c < nch) gram_first(k, N, c);
+                lds_barrier();
+            }
+        };
+        if (wave == C::W_GRAM) run(i0);
+        else run(i1);
+        drain();
         return;
     }
     // rows of O^T + (P U)^T of chunk c, scaled and stored: lane (r, g) holds token r of the
@@ -368,6 +387,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB, SAVE>::THREADS)) void gdn_prefill_ke
                 lds_barrier();
             }
             if (nch > 0) save_u(nch - 1);
+            drain();
             return;
         }
     }
@@ -413,6 +433,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB, SAVE>::THREADS)) void gdn_prefill_ke
             lds_barrier();
         }
         if (nch > 0) done(nch - 1);
+        drain();
         return;
     }
 
@@ -646,6 +667,7 @@ __global__ __launch_bounds__((GCfg<DK, NCB, SAVE>::THREADS)) void gdn_prefill_ke
         }
         lds_barrier();
     }
+    drain();
     if (a.Sf) {
 #pragma unroll
         for (int cb = 0; cb < CPW; ++cb)
