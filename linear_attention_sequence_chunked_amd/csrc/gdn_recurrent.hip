@@ -10,10 +10,9 @@
 // Two uses.  The step (1..16 tokens per sequence, the serving form): the state is the large
 // operand, read once and written once whatever the number of tokens; HBM-bound.  The
 // sequential prefill (any length, the form of 32-bit inputs): the state stays in registers
-// for the whole sequence and the tokens stream through LDS in blocks of 16, one barrier per
-// token; bound by that barrier and the two reductions (0.7 us a token at 64 x 128).
+// for the whole sequence and the tokens stream through LDS.
 //
-// A workgroup of four waves owns NV value columns of one state.  Thread t holds columns
+// The step: a workgroup of four waves owns NV value columns of one state.  Thread t holds columns
 // 4 (t % COLG) .. +3 of rows rg + ROWG i (rg = t / COLG): a row of the slice is read and written
 // by COLG consecutive threads as one contiguous segment, and the workgroup's accesses of one i
 // are one contiguous stretch of the state.  k and q lie in LDS in the order of the threads'
@@ -67,8 +66,7 @@ struct Tile {
     static __device__ constexpr int place(int row) { return row % ROWG * RPT + row / ROWG; }
 };
 
-// The tokens' rows on their way from memory to LDS: loaded before a block of tokens is
-// worked on, stored after it.
+// The tokens' rows on their way from memory to LDS.
 template <typename T, int DK, int DV, int NV, int TB>
 struct Stage {
     using L = Tile<DK, NV, TB>;
@@ -99,8 +97,8 @@ struct Stage {
     }
 };
 
-// one sequence's tokens from row0 on; `advance` tokens move the stored state (to Sout),
-// outputs are written where `out` is given
+// one sequence's n <= TB tokens from row0 on; the first `advance` move the stored state (to
+// Sout), outputs are written where `out` is given
 template <typename T, int DK, int DV, int NV, int TB>
 __device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t row0, int n,
                      int advance, T* out, int head, int col0, bool skip_check, int slot_seq) {
@@ -119,7 +117,7 @@ __device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t ro
     for (int i = 0; i < L::RPT; ++i)
         s[i] = Sin ? __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(Sin + at + i * STEP)) : zero4();
     Stage<T, DK, DV, NV, TB> st;
-    st.load(A, row0, min(n, TB), hk, head, col0);
+    st.load(A, row0, n, hk, head, col0);
     bool twice = false;  // an earlier row of this call names the same slot
     if (skip_check) {
         for (int j = t; j < slot_seq; j += kThreads) twice |= A.slots[j] == A.slots[slot_seq];
@@ -138,76 +136,70 @@ __device__ void walk(const RecArgs& A, const float* Sin, float* Sout, int64_t ro
         for (int i = 0; i < L::RPT; ++i)
             __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(Sout + at + i * STEP));
     };
-    if (advance == 0 && Sout != Sin) put();
-    for (int t0 = 0; t0 < n; t0 += TB) {
-        const int m = min(n - t0, TB);
-        __syncthreads();  // the block before is done with the tiles
 #pragma unroll
-        for (int i = 0; i < L::QV; ++i) {
-            const int e = t + kThreads * i, r = e / (DK / 4), c = 4 * (e % (DK / 4));
-            if (r < TB) {
+    for (int i = 0; i < L::QV; ++i) {
+        const int e = t + kThreads * i, r = e / (DK / 4), c = 4 * (e % (DK / 4));
+        if (r < TB) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    s_k[r][L::place(c + x)] = st.k[i][x];
-                    s_q[r][L::place(c + x)] = st.q[i][x] * A.scale;
-                }
+            for (int x = 0; x < 4; ++x) {
+                s_k[r][L::place(c + x)] = st.k[i][x];
+                s_q[r][L::place(c + x)] = st.q[i][x] * A.scale;
             }
         }
+    }
 #pragma unroll
-        for (int i = 0; i < L::VV; ++i) {
-            const int e = t + kThreads * i, r = e / (NV / 4), c = 4 * (e % (NV / 4));
-            if (r < TB) *reinterpret_cast<f32x4*>(&s_v[r][c]) = st.v[i];
+    for (int i = 0; i < L::VV; ++i) {
+        const int e = t + kThreads * i, r = e / (NV / 4), c = 4 * (e % (NV / 4));
+        if (r < TB) *reinterpret_cast<f32x4*>(&s_v[r][c]) = st.v[i];
+    }
+    if (t < TB) {
+        s_a[t] = expf(st.g);
+        s_b[t] = st.b;
+    }
+    __syncthreads();
+    if (out) {  // k . (scale q) of every token: 16 lanes each
+        float kq = 0.f;
+        const int tok = t / 16 % TB;
+#pragma unroll
+        for (int c = 0; c < DK / 16; ++c) kq = fmaf(s_k[tok][L::place(t % 16 + 16 * c)], s_q[tok][L::place(t % 16 + 16 * c)], kq);
+#pragma unroll
+        for (int off = 8; off >= 1; off >>= 1) kq += __shfl_xor(kq, off);
+        if (t % 16 == 0 && t / 16 < TB) s_kq[tok] = kq;  // read behind the next barrier
+    }
+    for (int j = 0; j < n; ++j) {
+        f32x4 w = zero4(), b = zero4();
+#pragma unroll
+        for (int i = 0; i < L::RPT; ++i) {
+            w = fma4(s_k[j][rg * L::RPT + i], s[i], w);
+            b = fma4(s_q[j][rg * L::RPT + i], s[i], b);
         }
-        if (t < TB) {
-            s_a[t] = expf(st.g);
-            s_b[t] = st.b;
+#pragma unroll
+        for (int off = L::COLG; off < 64; off <<= 1) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                w[c] += __shfl_xor(w[c], off);
+                b[c] += __shfl_xor(b[c], off);
+            }
+        }
+        if (lane < L::COLG) {
+            s_red[j & 1][wave][lane][0] = w;
+            s_red[j & 1][wave][lane][1] = b;
         }
         __syncthreads();
-        if (t0 + TB < n) st.load(A, row0 + t0 + TB, min(n - t0 - TB, TB), hk, head, col0);
-        if (out) {  // k . (scale q) of every token: 16 lanes each
-            float kq = 0.f;
-            const int tok = t / 16 % TB;
+        w = (s_red[j & 1][0][cg][0] + s_red[j & 1][1][cg][0]) +
+            (s_red[j & 1][2][cg][0] + s_red[j & 1][3][cg][0]);
+        b = (s_red[j & 1][0][cg][1] + s_red[j & 1][1][cg][1]) +
+            (s_red[j & 1][2][cg][1] + s_red[j & 1][3][cg][1]);
+        const float a = s_a[j];
+        const f32x4 u = s_b[j] * fma4(-a, w, *reinterpret_cast<const f32x4*>(&s_v[j][4 * cg]));
 #pragma unroll
-            for (int c = 0; c < DK / 16; ++c) kq = fmaf(s_k[tok][L::place(t % 16 + 16 * c)], s_q[tok][L::place(t % 16 + 16 * c)], kq);
-#pragma unroll
-            for (int off = 8; off >= 1; off >>= 1) kq += __shfl_xor(kq, off);
-            if (t % 16 == 0 && t / 16 < TB) s_kq[tok] = kq;  // read behind the next barrier
-        }
-        for (int j = 0; j < m; ++j) {
-            f32x4 w = zero4(), b = zero4();
-#pragma unroll
-            for (int i = 0; i < L::RPT; ++i) {
-                w = fma4(s_k[j][rg * L::RPT + i], s[i], w);
-                b = fma4(s_q[j][rg * L::RPT + i], s[i], b);
-            }
-#pragma unroll
-            for (int off = L::COLG; off < 64; off <<= 1) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    w[c] += __shfl_xor(w[c], off);
-                    b[c] += __shfl_xor(b[c], off);
-                }
-            }
-            if (lane < L::COLG) {
-                s_red[j & 1][wave][lane][0] = w;
-                s_red[j & 1][wave][lane][1] = b;
-            }
-            __syncthreads();
-            w = (s_red[j & 1][0][cg][0] + s_red[j & 1][1][cg][0]) +
-                (s_red[j & 1][2][cg][0] + s_red[j & 1][3][cg][0]);
-            b = (s_red[j & 1][0][cg][1] + s_red[j & 1][1][cg][1]) +
-                (s_red[j & 1][2][cg][1] + s_red[j & 1][3][cg][1]);
-            const float a = s_a[j];
-            const f32x4 u = s_b[j] * fma4(-a, w, *reinterpret_cast<const f32x4*>(&s_v[j][4 * cg]));
-#pragma unroll
-            for (int i = 0; i < L::RPT; ++i) s[i] = fma4(s_k[j][rg * L::RPT + i], u, a * s[i]);
-            if (out && rg == 0)
-                store4(out + (row0 + t0 + j) * (int64_t)A.hv * DV + (int64_t)head * DV + col0 + 4 * cg,
-                       Mma<T>::pack(fma4(s_kq[j], u, a * b)));
-            if (t0 + j + 1 == advance) {
-                put();
-                if (!out) return;  // (the whole workgroup: advance is the same for all)
-            }
+        for (int i = 0; i < L::RPT; ++i) s[i] = fma4(s_k[j][rg * L::RPT + i], u, a * s[i]);
+        if (out && rg == 0)
+            store4(out + (row0 + j) * (int64_t)A.hv * DV + (int64_t)head * DV + col0 + 4 * cg,
+                   Mma<T>::pack(fma4(s_kq[j], u, a * b)));
+        if (j + 1 == advance) {
+            put();
+            if (!out) return;  // (the whole workgroup: advance is the same for all)
         }
     }
 }
@@ -332,14 +324,129 @@ __global__ __launch_bounds__(kThreads, DK * NV == 128 * 128 ? 2 : 4) void decode
     if (out && rg == 0) store4(out + 4 * cg, Mma<T>::pack(fma4(kq, u, a * b)));  // (wave 0)
 }
 
-template <typename T, int DK, int DV, int NV>
+// The prefill of 32-bit inputs, token by token.  Each wave keeps eight columns of a state for the
+// whole sequence: lane (rg, cp) (rg = lane & 15) holds columns 2 cp, 2 cp + 1 of DK / 16
+// consecutive rows, so a column sum is four rotations within the 16 lanes of a DPP row and the
+// waves meet only once per 16 staged tokens (with a state's rows spread over four waves, as in
+// the step, the barrier and the shuffles through LDS take 0.73 us a token; this takes 0.22 at
+// dk = 64).  Narrow slices also spread few sequences over the card.  Bound by the dependent
+// chain of a token: two sums, the update, the next token's sums.
+template <int DK, int DV>
 __global__ __launch_bounds__(kThreads) void seq_kernel(const RecArgs A, const GdnTable tab) {
-    constexpr int SL = DV / NV;
+    constexpr int TB = 16, NV = 32, SL = DV / NV, R = DK / 16;
+    constexpr int QV = TB * DK / 4 / kThreads;
+    __shared__ __attribute__((aligned(16))) float s_k[2][TB][DK], s_q[2][TB][DK], s_v[2][TB][NV], s_o[2][TB][NV];
+    __shared__ float s_a[2][TB], s_b[2][TB];
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const int t = threadIdx.x, lane = t & 63, rg = lane & 15, cp = lane >> 4;
     const int64_t pair = blockIdx.x / SL;
-    const int i = (int)(pair / A.hv), head = (int)(pair % A.hv), col0 = NV * (int)(blockIdx.x % SL);
-    const int64_t ss = ((int64_t)tab.id[i] * A.hv + head) * (int64_t)(DK * DV);
-    walk<T, DK, DV, NV, 16>(A, A.S0 ? A.S0 + ss : nullptr, A.Sf ? A.Sf + ss : nullptr, tab.start[i],
-                        tab.len[i], tab.len[i], (T*)A.out, head, col0, false, 0);
+    const int i = (int)(pair / A.hv), head = (int)(pair % A.hv), hk = head / (A.hv / A.hk), col0 = NV * (int)(blockIdx.x % SL);
+    const int col = 8 * (t / 64) + 2 * cp;  // of the slice
+    const int64_t start = tab.start[i], ss = ((int64_t)tab.id[i] * A.hv + head) * (int64_t)(DK * DV);
+    const int len = tab.len[i];
+    const int64_t at = ss + (int64_t)rg * R * DV + col0 + col;
+    f32x2 s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        s[r] = A.S0 ? *reinterpret_cast<const f32x2*>(A.S0 + at + r * DV) : f32x2{0.f, 0.f};
+    // tokens on their way: rows of k and q, two entries of v, a gate
+    f32x4 rk[QV], rq[QV];
+    f32x2 rv;
+    float rg_ = 0.f, rb = 0.f;
+    const int vr = t / 16, vc = 2 * (t % 16);
+    auto load = [&](int t0) {
+#pragma unroll
+        for (int x = 0; x < QV; ++x) {
+            const int e = t + kThreads * x, row = e / (DK / 4), c = 4 * (e % (DK / 4));
+            rk[x] = rq[x] = zero4();
+            if (t0 + row < len) {
+                rk[x] = load4f((const float*)A.k + (start + t0 + row) * A.ks + (int64_t)hk * DK + c);
+                rq[x] = load4f((const float*)A.q + (start + t0 + row) * A.qs + (int64_t)hk * DK + c);
+            }
+        }
+        rv = f32x2{0.f, 0.f};
+        if (t0 + vr < len)
+            rv = *reinterpret_cast<const f32x2*>((const float*)A.v + (start + t0 + vr) * A.vs + (int64_t)head * DV + col0 + vc);
+        rg_ = rb = 0.f;
+        if (t < TB && t0 + t < len) {
+            rg_ = A.la[(start + t0 + t) * A.hv + head];
+            rb = A.be[(start + t0 + t) * A.hv + head];
+        }
+    };
+    auto put = [&](int b) {
+#pragma unroll
+        for (int x = 0; x < QV; ++x) {
+            const int e = t + kThreads * x, row = e / (DK / 4), c = 4 * (e % (DK / 4));
+            *reinterpret_cast<f32x4*>(&s_k[b][row][c]) = rk[x];
+            *reinterpret_cast<f32x4*>(&s_q[b][row][c]) = rq[x] * A.scale;
+        }
+        *reinterpret_cast<f32x2*>(&s_v[b][vr][vc]) = rv;
+        if (t < TB) {
+            s_a[b][t] = expf(rg_);
+            s_b[b][t] = rb;
+        }
+    };
+    auto sum16 = [](float x) {  // over the row of 16 lanes, in every lane
+        x += dpp<0x128>(x);
+        x += dpp<0x124>(x);
+        x += dpp<0x122>(x);
+        x += dpp<0x121>(x);
+        return x;
+    };
+    load(0);
+    for (int t0 = 0; t0 < len; t0 += TB) {
+        const int b = (t0 / TB) & 1, m = min(len - t0, TB);
+        put(b);
+        lds_barrier();
+        if (t0 > 0) {  // the block before: whole rows of the slice
+            *reinterpret_cast<f32x2*>((float*)A.out + ((start + t0 - TB + vr) * A.hv + head) * (int64_t)DV + col0 + vc) =
+                *reinterpret_cast<const f32x2*>(&s_o[1 - b][vr][vc]);
+        }
+        load(t0 + TB);
+        for (int j = 0; j < m; ++j) {
+            float k[R], q[R];
+#pragma unroll
+            for (int r = 0; r < R; r += 4) {
+                const f32x4 kk = *reinterpret_cast<const f32x4*>(&s_k[b][j][rg * R + r]);
+                const f32x4 qq = *reinterpret_cast<const f32x4*>(&s_q[b][j][rg * R + r]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    k[r + x] = kk[x];
+                    q[r + x] = qq[x];
+                }
+            }
+            f32x2 w = {0.f, 0.f}, o = {0.f, 0.f};
+            float kq = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                w += s[r] * k[r];
+                o += s[r] * q[r];
+                kq = fmaf(k[r], q[r], kq);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                w[c] = sum16(w[c]);
+                o[c] = sum16(o[c]);
+            }
+            kq = sum16(kq);
+            const float a = s_a[b][j];
+            const f32x2 u = s_b[b][j] * (*reinterpret_cast<const f32x2*>(&s_v[b][j][col]) - a * w);
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r] = a * s[r] + k[r] * u;
+            if (rg == 0) *reinterpret_cast<f32x2*>(&s_o[b][j][col]) = a * o + kq * u;
+        }
+    }
+    lds_barrier();
+    if (len > 0) {  // the last block's outputs
+        const int t0 = (len - 1) / TB * TB;
+        if (t0 + vr < len)
+            *reinterpret_cast<f32x2*>((float*)A.out + ((start + t0 + vr) * A.hv + head) * (int64_t)DV + col0 + vc) =
+                *reinterpret_cast<const f32x2*>(&s_o[(t0 / TB) & 1][vr][vc]);
+    }
+    if (A.Sf) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) *reinterpret_cast<f32x2*>(A.Sf + at + r * DV) = s[r];
+    }
 }
 
 // f(T, DK, DV, NV) for the call's type and shapes
@@ -394,14 +501,15 @@ hipError_t launch_gdn_sequential(const GdnPrefillArgs& a, const GdnTable& tab, h
     RecArgs r = common(a.d);
     r.q = a.q; r.k = a.k; r.v = a.v; r.la = a.log_alpha; r.be = a.beta; r.out = a.out;
     r.S0 = a.initial_state; r.Sf = a.final_state;
-    const int64_t blocks = (int64_t)a.num_seqs * a.d.hv * (a.d.dv / a.nv);
+    const int64_t blocks = (int64_t)a.num_seqs * a.d.hv * (a.d.dv / 32);
+    if (a.d.dtype != DTYPE_F32) return hipErrorInvalidValue;
     if (blocks == 0) return hipSuccess;
-    return dispatch(a.d, a.nv, [&](auto t, auto dk, auto dv, auto nv) {
-        hipLaunchKernelGGL((seq_kernel<decltype(t), decltype(dk)::value, decltype(dv)::value,
-                                       decltype(nv)::value>),
-                           dim3((unsigned)blocks), dim3(kThreads), 0, stream, r, tab);
-        return hipGetLastError();
-    });
+    const dim3 grid((unsigned)blocks), block(kThreads);
+    if (a.d.dk == 128 && a.d.dv == 128) hipLaunchKernelGGL((seq_kernel<128, 128>), grid, block, 0, stream, r, tab);
+    else if (a.d.dk == 128) hipLaunchKernelGGL((seq_kernel<128, 64>), grid, block, 0, stream, r, tab);
+    else if (a.d.dv == 128) hipLaunchKernelGGL((seq_kernel<64, 128>), grid, block, 0, stream, r, tab);
+    else hipLaunchKernelGGL((seq_kernel<64, 64>), grid, block, 0, stream, r, tab);
+    return hipGetLastError();
 }
 
 }  // namespace kda
