@@ -491,32 +491,47 @@ __global__ __launch_bounds__((GCfg<DK, NCB, SAVE>::THREADS)) void gdn_prefill_ke
         for (int cb = 0; cb < CPW; ++cb)
 #pragma unroll
             for (int t = 0; t < 4; ++t) Y[cb][t] = O[cb][t] = zero4();
+        // The conversions of step p + 1 are issued between the products of step p: the vector unit works under the matrix
+        // unit's time (one sequence of 131072 tokens, 32 heads: 3.76 ms; in front of the products 3.87).
+        f16x8 sh[2][CPW], sl[2][CPW];
+        auto split_state = [&](auto PI) {
+            constexpr int p = decltype(PI)::value;
+#pragma unroll
+            for (int cb = 0; cb < CPW; ++cb) split8(S[cb][2 * p], S[cb][2 * p + 1], sh[p % 2][cb], sl[p % 2][cb], m1);
+        };
+        split_state(i0);
         unroll<0, KP>([&](auto PI) {
             constexpr int p = decltype(PI)::value, k = p % 2;
             if constexpr (p + 1 < KP) {
                 load_k(kf[1 - k], c, p + 1);
                 if constexpr (!C::NARROW) load_q(qf[1 - k], c, p + 1);
-                __builtin_amdgcn_sched_barrier(0);
             }
-            f16x8 sh[CPW], sl[CPW];
-#pragma unroll
-            for (int cb = 0; cb < CPW; ++cb) split8(S[cb][2 * p], S[cb][2 * p + 1], sh[cb], sl[cb], m1);
-            if constexpr (C::NARROW) lds_st(xw + C::X_S + p * C::FR, sh[0]);
-            if constexpr (SAVE) lds_st(xw + C::X_S + (KP + p) * C::FR, sl[0]);
+            if constexpr (C::NARROW) lds_st(xw + C::X_S + p * C::FR, sh[k][0]);
+            if constexpr (SAVE) lds_st(xw + C::X_S + (KP + p) * C::FR, sl[k][0]);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (p + 1 < KP) split_state(integral_constant<int, p + 1>{});
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int cb = 0; cb < CPW; ++cb) Y[cb][t] = mfma32h(kf[k][t], sh[cb], Y[cb][t]);
+                for (int cb = 0; cb < CPW; ++cb) Y[cb][t] = mfma32h(kf[k][t], sh[k][cb], Y[cb][t]);
             if constexpr (!C::NARROW) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int cb = 0; cb < CPW; ++cb) O[cb][t] = mfma32h(sh[cb], qf[k][t], O[cb][t]);
+                    for (int cb = 0; cb < CPW; ++cb) O[cb][t] = mfma32h(sh[k][cb], qf[k][t], O[cb][t]);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int cb = 0; cb < CPW; ++cb) Y[cb][t] = mfma32h(kf[k][t], sl[cb], Y[cb][t]);
+                for (int cb = 0; cb < CPW; ++cb) Y[cb][t] = mfma32h(kf[k][t], sl[k][cb], Y[cb][t]);
+            if constexpr (p + 1 < KP) {
+#pragma unroll
+                for (int n = 0; n < CPW * (C::NARROW ? 8 : 12); ++n) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // a product
+                    __builtin_amdgcn_sched_group_barrier(0x002, C::NARROW ? 2 : 1, 0);  // a conversion or two
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
         });
         __builtin_amdgcn_sched_barrier(0);  // the products stay in this phase
         lds_barrier();
