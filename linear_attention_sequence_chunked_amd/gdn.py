@@ -31,7 +31,10 @@ def _tokens(name, t, heads, d, dtype, device):
         raise ValueError(f"{name}: tokens must be a fixed stride apart (strides {st})")
     if t.numel() == 0 or shape[:-2].numel() == 1:
         return heads * d  # no second token to stride to
-    return st[0] if len(shape) == 4 and shape[1] == 1 else st[-3]
+    stride = st[0] if len(shape) == 4 and shape[1] == 1 else st[-3]
+    if stride < heads * d:  # (0, an expanded tensor's, would mean dense)
+        raise ValueError(f"{name}: tokens overlap (strides {st})")
+    return stride
 
 
 def _dense(name, t, shape, dtype, device):

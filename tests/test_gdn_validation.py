@@ -153,6 +153,20 @@ def test_binding_token_strides(on_cpu):
         gdn._tokens("q", w.view(2, 3, 512)[:, :2, :128].view(2, 2, 2, 64), 2, 64, w.dtype, dev)
 
 
+def test_binding_refuses_overlapping_tokens(on_cpu):
+    """A token stride of 0 (an expanded tensor) must not reach the library, where 0 means dense."""
+    one = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    for t in (one.expand(6, 2, 64), one[None].expand(3, 2, 2, 64), one[None].expand(6, 1, 2, 64), torch.zeros(512, dtype=torch.bfloat16).as_strided((6, 2, 64), (64, 64, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            gdn._tokens("q", t, 2, 64, t.dtype, t.device)
+    x = tensors()
+    for name in ("q", "k", "v"):
+        with pytest.raises(ValueError, match="overlap"):
+            gdn.gdn_chunk_prefill(**dict(x, **{name: x[name][:1].expand_as(x[name])}), cu_seqlens=[0, 6])
+        with pytest.raises(ValueError, match="overlap"):
+            gdn.gdn_recurrent(**dict(x, **{name: x[name][:1].expand_as(x[name])}), state=torch.zeros(6, 4, 64, 64))
+
+
 def test_binding_recurrent_refusals(on_cpu):
     x = tensors()
     st = torch.zeros(8, 4, 64, 64)
