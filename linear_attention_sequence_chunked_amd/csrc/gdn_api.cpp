@@ -66,10 +66,16 @@ uint64_t extent(int64_t tokens, int64_t stride, int64_t row, size_t es) {
     return tokens > 0 ? ((uint64_t)(tokens - 1) * stride + row) * es : 0;
 }
 
-kda_status check_grid(int64_t blocks) {
-    if (blocks > INT32_MAX)
+// a grid's threads are counted in 32 bits
+kda_status check_grid(int64_t blocks, int64_t threads) {
+    if (blocks > UINT32_MAX / threads)
         return fail(KDA_ERR_UNSUPPORTED, "%lld workgroups exceed one launch", (long long)blocks);
     return KDA_OK;
+}
+
+// the (sequence, head) pairs of one launch, their columns cut finest, at most 1024 threads each
+kda_status check_pairs(const kda::GdnDims& d, int32_t num_seqs) {
+    return check_grid((int64_t)std::min(num_seqs, kda::kGdnSeqs) * d.hv * (d.dv / 16) + 64, 1024);
 }
 
 kda_status check_cu(const int32_t* cu, int32_t n) {
@@ -215,9 +221,9 @@ kda_status kda_gdn_prefill_backward(const kda_gdn_params* params, const void* q,
                 if (overlaps(outs[i], outs[j]))
                     return fail(KDA_ERR_INVALID_ARGUMENT, "%s overlaps %s", outs[i].name, outs[j].name);
         }
-        if ((st = check_grid(std::min<int64_t>(num_seqs, kda::kGdnSeqs) * d.hv * (d.dv / 16))) != KDA_OK) return st;
-        if ((st = check_grid(T * d.hk * (d.dk / 4) / 256 + 1)) != KDA_OK) return st;
-        if ((st = check_grid((T / 64 + 1) * d.hv)) != KDA_OK) return st;
+        if ((st = check_pairs(d, num_seqs)) != KDA_OK) return st;
+        if ((st = check_grid(T * d.hk * (d.dk / 4) / 256 + 1, 256)) != KDA_OK) return st;
+        if ((st = check_grid((T / 64 + 1) * d.hv, 256)) != KDA_OK) return st;
         a.T = T; a.q = q; a.k = k; a.v = v; a.d_out = d_out; a.log_alpha = log_alpha; a.beta = beta;
         a.initial_state = initial_state; a.d_final_state = d_final_state; a.dq = dq; a.dk = dk; a.dv = dv;
         a.dlog_alpha = dlog_alpha; a.dbeta = dbeta; a.d_initial_state = d_initial_state;
@@ -278,7 +284,7 @@ kda_status kda_gdn_chunk_prefill(const kda_gdn_params* params, const void* q, co
             return fail(KDA_ERR_INVALID_ARGUMENT, "final_state overlaps initial_state");
         const int cus = kda::device_cu_count();
         const int64_t pairs = (int64_t)num_seqs * d.hv;
-        if ((st = check_grid(std::min<int64_t>(num_seqs, kda::kGdnSeqs) * d.hv * (d.dv / 16))) != KDA_OK) return st;
+        if ((st = check_pairs(d, num_seqs)) != KDA_OK) return st;
         a.q = q; a.k = k; a.v = v; a.log_alpha = log_alpha; a.beta = beta;
         a.initial_state = initial_state; a.final_state = final_state; a.out = out;
         const bool chunked = d.dtype == KDA_DTYPE_BF16;
@@ -334,7 +340,7 @@ kda_status kda_gdn_recurrent(const kda_gdn_params* params, const void* q, const 
         if (overlaps(ro, r)) return fail(KDA_ERR_INVALID_ARGUMENT, "out overlaps %s", r.name);
         if (update_state && overlaps(rs, r)) return fail(KDA_ERR_INVALID_ARGUMENT, "state overlaps %s", r.name);
     }
-    if ((st = check_grid((int64_t)num_seqs * d.hv * (d.dv / 32))) != KDA_OK) return st;
+    if ((st = check_grid((int64_t)num_seqs * d.hv * (d.dv / 32), 256)) != KDA_OK) return st;
     a.num_seqs = num_seqs; a.num_tokens = num_tokens; a.num_slots = num_slots;
     a.q = q; a.k = k; a.v = v; a.log_alpha = log_alpha; a.beta = beta; a.steps = steps;
     a.state_indices = state_indices; a.state = state; a.update = update_state != 0; a.out = out;
@@ -401,7 +407,7 @@ kda_status kda_spec_accept(int32_t dtype, int32_t num_seqs, int32_t num_draft, i
     a.partial = static_cast<double*>(workspace);
     a.pieces = kda::accept_pieces(num_seqs, vocab, kda::device_cu_count());
     a.piece = (vocab + a.pieces - 1) / a.pieces;
-    if ((st = check_grid((int64_t)num_seqs * a.pieces)) != KDA_OK) return st;
+    if ((st = check_grid((int64_t)num_seqs * a.pieces, 256)) != KDA_OK) return st;
     const hipError_t e = kda::launch_accept(a, reinterpret_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(KDA_ERR_HIP, "kda_spec_accept launch: %s", hipGetErrorString(e));
     return kda::ok();

@@ -107,6 +107,16 @@ def test_accept_workspace_sizes():
     assert accept(n=0)[0] == _lib.KDA_OK
 
 
+def test_launches_beyond_the_grid_are_refused():
+    """2^24 states of one launch: more threads than a grid counts."""
+    p = params(hk=1, hv=1 << 16, dv=128)
+    st, msg = prefill(p, cu=[0] * 257, n=256, q=None, k=None, v=None, la=None, be=None, out=None)
+    assert st == UNS and "workgroups exceed one launch" in msg
+    far = dict(q=1 << 54, k=1 << 55, v=1 << 56, la=1 << 57, be=1 << 58, out=1 << 59)
+    st, msg = recurrent(p, n=1 << 12, slots=0, idx=1 << 53, state=None, upd=0, **far)
+    assert st == UNS and "workgroups exceed one launch" in msg
+
+
 # ------------------------------------------------------------------------------ the binding
 
 @pytest.fixture
