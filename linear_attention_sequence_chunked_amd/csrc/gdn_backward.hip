@@ -431,11 +431,11 @@ struct GradCfg {
 };
 
 template <int DK, int DV>
-__global__ __launch_bounds__(256, 2) void gdn_gradients_kernel(const GdnBackwardArgs A, const GdnTable tab) {
+__global__ __launch_bounds__(256, 2) void gdn_gradients_kernel(const GdnBackwardArgs A, const GdnTable tab, int from) {
     typedef GradCfg<DK> C;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const GdnDims& d = A.d;
-    const int si = blockIdx.y, len = tab.len[si], nch = (len + kGC - 1) / kGC;
+    const int si = from + blockIdx.y, len = tab.len[si], nch = (len + kGC - 1) / kGC;
     const int h = blockIdx.x % d.hv, c = blockIdx.x / d.hv;
     if (c >= nch) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -839,14 +839,20 @@ hipError_t walk_back(const GdnBackwardArgs& p, const GdnTable& tab, hipStream_t 
 
 template <int DK, int DV>
 hipError_t gradients(const GdnBackwardArgs& p, const GdnTable& tab, hipStream_t st) {
-    const int chunks = (tab.len[0] + kGC - 1) / kGC;  // of the longest sequence
-    if (chunks == 0) return hipSuccess;
     constexpr int lds = GradCfg<DK>::LDS_BYTES;
     hipError_t e = hipFuncSetAttribute((const void*)gdn_gradients_kernel<DK, DV>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gdn_gradients_kernel<DK, DV>), dim3((unsigned)(chunks * p.d.hv), (unsigned)p.num_seqs), dim3(256), lds, st, p,
-                       tab);
-    return hipGetLastError();
+    for (int from = 0; from < p.num_seqs;) {
+        const int n = gdn_gradient_group(tab, from, p.num_seqs, p.d.hv);
+        if (n == 0) break;
+        const int chunks = (tab.len[from] + kGC - 1) / kGC;  // of the group's longest
+        hipLaunchKernelGGL((gdn_gradients_kernel<DK, DV>), dim3((unsigned)(chunks * p.d.hv), (unsigned)n), dim3(256), lds, st, p, tab,
+                           from);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        from += n;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

@@ -91,6 +91,9 @@ int gdn_recurrent_nv(int dv, int64_t pairs, int tokens, int cu_count);
 int gdn_prefill_nv(int dv, int64_t pairs, int cu_count);
 // value columns per workgroup of the backward's walks (gdn_plan.cpp)
 int gdn_backward_nv(int dv, int64_t pairs, int cu_count);
+// sequences from place `from` of a table (longest first) on that share a launch of the chunks'
+// gradients; 0: none of them has a token (gdn_plan.cpp)
+int gdn_gradient_group(const GdnTable& t, int from, int n, int hv);
 // pieces the vocabulary of one sequence is cut into (gdn_plan.cpp)
 int accept_pieces(int64_t num_seqs, int64_t vocab, int cu_count);
 

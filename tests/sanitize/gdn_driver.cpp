@@ -91,6 +91,24 @@ int main() {
             expect(kda_spec_accept(KDA_DTYPE_F32, n, n == 300 ? 0 : 4, v, (void*)(1ull << 52), nullptr, in(3), fl(4), nullptr,
                                    in(5), in(6), at(7), ws, nullptr), KDA_ERR_HIP, "accept");
         }
+    // groups of a launch: in order, every sequence with tokens once, few workgroups without a chunk
+    for (int spread : {1, 7, 900, 100000}) {
+        kda::GdnTable t;
+        for (int i = 0; i < kda::kGdnSeqs; ++i) t.len[i] = (kda::kGdnSeqs - 10 - i) * spread / 9;
+        for (int i = kda::kGdnSeqs - 10; i < kda::kGdnSeqs; ++i) t.len[i] = 0;
+        t.len[0] += 50 * spread;
+        int from = 0;
+        while (from < kda::kGdnSeqs) {
+            const int n = kda::gdn_gradient_group(t, from, kda::kGdnSeqs, 4);
+            if (n == 0) break;
+            long long work = 0;
+            for (int i = from; i < from + n; ++i) work += (t.len[i] + 63) / 64 * 4;
+            const long long grid = (t.len[from] + 63) / 64 * 4ll * n;
+            expect(n > 0 && grid - work <= 32768 + work, 1, "a group's empty workgroups");
+            from += n;
+        }
+        for (int i = from; i < kda::kGdnSeqs; ++i) expect(t.len[i], 0, "no sequence with tokens is left out");
+    }
     std::printf("%d unexpected results\n", bad);
     return bad != 0;
 }

@@ -74,6 +74,12 @@ def test_backward_many_sequences(dtype):
     check(x, cu, DT[dtype])
 
 
+def test_backward_one_long_sequence_among_short_ones():
+    """Lengths so far apart that the chunks' gradients take several launches."""
+    x, cu = ref.inputs([3] * 150 + [700, 0] + [2] * 100 + [65], 1, 16, 64, 64, torch.bfloat16, seed=10)
+    check(x, cu, torch.bfloat16)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_backward_all_empty(dtype):
     x, cu = ref.inputs([0, 0], 1, 2, 64, 64, DT[dtype], seed=3)
