@@ -7,13 +7,18 @@
 //   dk = D u - A (beta du)      dbeta = du . err            dv = beta du
 //   D -= k (beta du)^T          dg = <D, A>                 D <- e^{g} D
 // A walk forwards keeps the state before every 16th token; backwards, each block of 16 is run
-// again from there with its decayed states A written to a scratch (L2-resident: 1 MiB per
-// workgroup), so no state is ever divided by its decay.  Everything is fp32.
+// again from there with its decayed states A written to a scratch (1 MiB per workgroup, the next
+// token's read during this one's sums), so no state is ever divided by its decay.  Everything is
+// fp32.
 //
 // One workgroup of four waves holds a whole state: thread t has columns 4 (t % COLG) .. +3 of
 // RPT consecutive rows.  Column sums (du) go through LDS, one barrier per token; row sums
-// (dq, dk) are reduced among the COLG threads of a row group, halving the rows at each step.
-// Bound by those reductions and the barrier (latency), not by memory.
+// (dq, dk) are reduced among the COLG threads of a row group, halving the rows at each step; the
+// gates' sums over the state (dg, dbeta) are kept per thread and added once per block.
+// States of 128 x 128: 4.3 us a token, of which about 2.5 are the issue of some 1500 vector
+// instructions by each of the four SIMDs (two walks forwards, one backwards), the rest LDS and
+// barriers; 6.6 with a state on each of 256 compute units, where the scratch's 128 KiB a token
+// come from beyond L2 at 5 TB/s.
 //
 // Heads that share a key head write their parts of dq and dk apart; a second launch adds them
 // in head order.
@@ -22,6 +27,7 @@
 #include "gdn_launch.h"
 #include "kda_device.h"
 #include "kda_launch.h"
+#include "kda_mfma.h"
 
 namespace kda {
 namespace {
@@ -30,42 +36,65 @@ constexpr int kThreads = 256;
 constexpr int TB = 16;
 
 __device__ inline f32x4 load4f(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
-__device__ inline f32x4 load4f(const bf16* p) { return __builtin_convertvector(*reinterpret_cast<const bf16x4*>(p), f32x4); }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 struct Shape {
     static constexpr int COLG = DV / 4, ROWG = kThreads / COLG, RPT = DK / ROWG;
     static constexpr int64_t STATE = (int64_t)DK * DV;
 };
 
-// sums over the COLG threads of a row group of RPT values each: thread c returns the sum of
-// value `row` (set for c < RPT's share, see use)
-template <int N, int LANES>
-__device__ inline float reduce_rows(float (&v)[N], int c, int& row) {
-    row = 0;
-    int off = 1;
-#pragma unroll
-    for (int n = N; n > 1; n /= 2) {
-        const bool up = c & off;
-#pragma unroll
-        for (int i = 0; i < n / 2; ++i) {
-            const float keep = up ? v[i + n / 2] : v[i], give = up ? v[i] : v[i + n / 2];
-            v[i] = keep + __shfl_xor(give, off);
-        }
-        row += up ? n / 2 : 0;
-        off *= 2;
-    }
-#pragma unroll
-    for (; off < LANES; off *= 2) v[0] += __shfl_xor(v[0], off);
-    return v[0];
+// x of the lane whose number differs in bit OFF: one DPP move, or a trip through LDS for 4 and 16
+template <int OFF>
+__device__ inline float partner(float x) {
+    if constexpr (OFF == 1) return dpp<0xB1>(x);
+    else if constexpr (OFF == 2) return dpp<0x4E>(x);
+    else if constexpr (OFF == 8) return dpp<0x128>(x);
+    else return __shfl_xor(x, OFF);
 }
 
-template <typename T, int DK, int DV>
+// Sums over LANES neighbouring threads of N values each, halving the values at each step: a
+// thread returns the sum of value `row`, chosen by the lane bits that the halvings took
+// (kTaken<N>).  (A recursion: in a loop whose bound halves the compiler keeps the array's indexes
+// dynamic, a select per element and access, which took 8.7 of 13.5 us a token.)
+constexpr int kOff[5] = {1, 2, 8, 4, 16};  // the moves first
+template <int N>
+constexpr int kTaken = N == 16 ? 15 : N == 8 ? 11 : 3;
+template <int N, int LANES, int STEP = 0>
+__device__ inline float reduce_rows(const float (&v)[N], int c, int& row) {
+    constexpr int OFF = kOff[STEP < 5 ? STEP : 0];
+    if constexpr (N == 1) {
+        if constexpr (STEP == 5 || (1 << STEP) == LANES) return v[0];
+        else {
+            const float x[1] = {v[0] + partner<OFF>(v[0])};
+            return reduce_rows<1, LANES, STEP + 1>(x, c, row);
+        }
+    } else {
+        const bool up = c & OFF;
+        float h[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float keep = up ? v[i + N / 2] : v[i], give = up ? v[i] : v[i + N / 2];
+            h[i] = keep + partner<OFF>(give);
+        }
+        row += up ? N / 2 : 0;
+        return reduce_rows<N / 2, LANES, STEP + 1>(h, c, row);
+    }
+}
+
+__device__ inline float sum16(float x) {  // over the row of 16 lanes
+    x += dpp<0x128>(x);
+    x += dpp<0x124>(x);
+    x += dpp<0x122>(x);
+    x += dpp<0x121>(x);
+    return x;
+}
+
+template <int DK, int DV>
 __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArgs A, const GdnTable tab, int pairs) {
-    using L = Shape<T, DK, DV>;
+    using L = Shape<DK, DV>;
     constexpr int COLG = L::COLG, RPT = L::RPT;
-    __shared__ __attribute__((aligned(16))) float s_k[TB][DK], s_q[TB][DK], s_v[TB][DV], s_do[TB][DV];
-    __shared__ float s_a[TB], s_b[TB], s_g[TB][4];
+    __shared__ __attribute__((aligned(16))) float s_k[TB][DK], s_q[TB][DK], s_v[TB][DV], s_do[TB][DV], s_err[TB][DV];
+    __shared__ float s_a[TB], s_b[TB], s_g[TB][kThreads], s_db[TB][COLG];
     __shared__ f32x4 s_red[2][4][COLG];
     const int t = threadIdx.x, cg = t % COLG, rg = t / COLG, wave = t / 64, lane = t % 64;
     float* scratch = A.scratch + (int64_t)blockIdx.x * TB * L::STATE;
@@ -82,13 +111,13 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
         auto stage = [&](int b) {
             const int m = min(TB, len - TB * b);
             const int64_t row0 = start + (int64_t)TB * b;
-            __syncthreads();
+            lds_barrier();
             for (int e = t; e < TB * DK / 4; e += kThreads) {
                 const int r = e / (DK / 4), c = 4 * (e % (DK / 4));
                 f32x4 kv = zero4(), qv = zero4();
                 if (r < m) {
-                    kv = load4f((const T*)A.k + (row0 + r) * d.ks + (int64_t)hk * DK + c);
-                    qv = load4f((const T*)A.q + (row0 + r) * d.qs + (int64_t)hk * DK + c);
+                    kv = load4f((const float*)A.k + (row0 + r) * d.ks + (int64_t)hk * DK + c);
+                    qv = load4f((const float*)A.q + (row0 + r) * d.qs + (int64_t)hk * DK + c);
                 }
                 *reinterpret_cast<f32x4*>(&s_k[r][c]) = kv;
                 *reinterpret_cast<f32x4*>(&s_q[r][c]) = qv * d.scale;
@@ -97,8 +126,8 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
                 const int r = e / (DV / 4), c = 4 * (e % (DV / 4));
                 f32x4 vv = zero4(), ov = zero4();
                 if (r < m) {
-                    vv = load4f((const T*)A.v + (row0 + r) * d.vs + (int64_t)h * DV + c);
-                    ov = load4f((const T*)A.d_out + ((row0 + r) * d.hv + h) * (int64_t)DV + c);
+                    vv = load4f((const float*)A.v + (row0 + r) * d.vs + (int64_t)h * DV + c);
+                    ov = load4f((const float*)A.d_out + ((row0 + r) * d.hv + h) * (int64_t)DV + c);
                 }
                 *reinterpret_cast<f32x4*>(&s_v[r][c]) = vv;
                 *reinterpret_cast<f32x4*>(&s_do[r][c]) = ov;
@@ -107,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
                 s_a[t] = expf(A.log_alpha[(row0 + t) * d.hv + h]);
                 s_b[t] = A.beta[(row0 + t) * d.hv + h];
             }
-            __syncthreads();
+            lds_barrier();
             return m;
         };
         int turn = 0;
@@ -118,7 +147,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
 #pragma unroll
                 for (int c = 0; c < 4; ++c) w[c] += __shfl_xor(w[c], off);
             if (lane < COLG) s_red[turn][wave][lane] = w;
-            __syncthreads();
+            lds_barrier();
             w = (s_red[turn][0][cg] + s_red[turn][1][cg]) + (s_red[turn][2][cg] + s_red[turn][3][cg]);
             turn ^= 1;
             return w;
@@ -139,10 +168,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
                 const f32x4 err = *reinterpret_cast<const f32x4*>(&s_v[j][4 * cg]) - w;
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) S[i] += s_k[j][rg * RPT + i] * (s_b[j] * err);
-                if (save) {
-                    __syncthreads();  // every row group has read v
-                    if (rg == 0) *reinterpret_cast<f32x4*>(&s_v[j][4 * cg]) = err;
-                }
+                if (save && rg == 0) *reinterpret_cast<f32x4*>(&s_err[j][4 * cg]) = err;
             }
         };
 #pragma unroll
@@ -162,12 +188,15 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
 #pragma unroll
             for (int i = 0; i < RPT; ++i) S[i] = *reinterpret_cast<const f32x4*>(keep + b * L::STATE + at + i * DV);
             forward(m, true);
-            __syncthreads();
-            for (int j = m - 1; j >= 0; --j) {
+            lds_barrier();
+            auto decayed = [&](int j) {
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) S[i] = *reinterpret_cast<const f32x4*>(scratch + j * L::STATE + at + i * DV);
+            };
+            decayed(m - 1);
+            for (int j = m - 1; j >= 0; --j) {
                 const float a = s_a[j], be = s_b[j];
-                const f32x4 err = *reinterpret_cast<const f32x4*>(&s_v[j][4 * cg]), u = be * err;
+                const f32x4 err = *reinterpret_cast<const f32x4*>(&s_err[j][4 * cg]), u = be * err;
                 const f32x4 go = *reinterpret_cast<const f32x4*>(&s_do[j][4 * cg]);
                 float pq[RPT], pk[RPT];
                 f32x4 w = zero4();
@@ -189,38 +218,46 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
                     dg += dot(D[i], S[i]);
                     D[i] *= a;
                 }
-                int row;
-                const float rq = reduce_rows<RPT, COLG>(pq, cg, row), rk = reduce_rows<RPT, COLG>(pk, cg, row);
-                if (cg < RPT) {
+                if (j > 0) decayed(j - 1);  // on their way during the sums over rows
+                int row = 0, same = 0;
+                const float rq = reduce_rows<RPT, COLG>(pq, cg, row), rk = reduce_rows<RPT, COLG>(pk, cg, same);
+                if ((cg & ~kTaken<RPT>) == 0) {
                     const int64_t o = (A.parts ? ((row0 + j) * d.hv + h) : ((row0 + j) * d.hk + hk)) * (int64_t)DK + rg * RPT + row;
                     if (A.parts) {
                         A.dq_parts[o] = d.scale * rq;
                         A.dk_parts[o] = rk;
                     } else {
-                        ((T*)A.dq)[o] = from_f32<T>(d.scale * rq);
-                        ((T*)A.dk)[o] = from_f32<T>(rk);
+                        ((float*)A.dq)[o] = d.scale * rq;
+                        ((float*)A.dk)[o] = rk;
                     }
                 }
-                const float db = dot(du, err);
-                float sum = db;
-#pragma unroll
-                for (int off = 1; off < COLG; off <<= 1) sum += __shfl_xor(sum, off);
+                s_g[j][t] = dg;  // summed over the threads behind the block
                 if (rg == 0) {
-                    store4((T*)A.dv + ((row0 + j) * d.hv + h) * (int64_t)DV + 4 * cg, Mma<T>::pack(bdu));
-                    if (cg == 0) A.dbeta[(row0 + j) * d.hv + h] = sum;
+                    *reinterpret_cast<f32x4*>((float*)A.dv + ((row0 + j) * d.hv + h) * (int64_t)DV + 4 * cg) = bdu;
+                    s_db[j][cg] = dot(du, err);
                 }
-#pragma unroll
-                for (int off = 1; off < 64; off <<= 1) dg += __shfl_xor(dg, off);
-                if (lane == 0) s_g[j][wave] = dg;
             }
-            __syncthreads();
-            if (t < m) A.dlog_alpha[(row0 + t) * d.hv + h] = (s_g[t][0] + s_g[t][1]) + (s_g[t][2] + s_g[t][3]);
+            lds_barrier();
+            {
+                const int j = t / 16, l = t % 16;
+                float x = 0.f, y = 0.f;
+#pragma unroll
+                for (int i = 0; i < kThreads / 16; ++i) x += s_g[j][l + 16 * i];
+#pragma unroll
+                for (int i = 0; i < COLG / 16; ++i) y += s_db[j][l + 16 * i];
+                x = sum16(x);
+                y = sum16(y);
+                if (l == 0 && j < m) {
+                    A.dlog_alpha[(row0 + j) * d.hv + h] = x;
+                    A.dbeta[(row0 + j) * d.hv + h] = y;
+                }
+            }
         }
         if (A.d_initial_state) {
 #pragma unroll
             for (int i = 0; i < RPT; ++i) *reinterpret_cast<f32x4*>(A.d_initial_state + ss + at + i * DV) = D[i];
         }
-        __syncthreads();
+        lds_barrier();
     }
 }
 
@@ -249,24 +286,20 @@ hipError_t sum_parts(const GdnBackwardArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 hipError_t launch(const GdnBackwardArgs& a, const GdnTable& tab, hipStream_t st) {
     const int pairs = a.num_seqs * a.d.hv;
     if (pairs == 0) return hipSuccess;
-    hipLaunchKernelGGL((backward_kernel<T, DK, DV>), dim3((unsigned)std::min(pairs, a.slots)), dim3(kThreads), 0, st, a, tab, pairs);
+    hipLaunchKernelGGL((backward_kernel<DK, DV>), dim3((unsigned)std::min(pairs, a.slots)), dim3(kThreads), 0, st, a, tab, pairs);
     return hipGetLastError();
-}
-
-template <typename T>
-hipError_t dispatch(const GdnBackwardArgs& a, const GdnTable& tab, hipStream_t st) {
-    if (a.d.dk == 128) return a.d.dv == 128 ? launch<T, 128, 128>(a, tab, st) : launch<T, 128, 64>(a, tab, st);
-    return a.d.dv == 128 ? launch<T, 64, 128>(a, tab, st) : launch<T, 64, 64>(a, tab, st);
 }
 
 }  // namespace
 
 hipError_t launch_gdn_backward_seq(const GdnBackwardArgs& a, const GdnTable& tab, hipStream_t st) {
-    return a.d.dtype == DTYPE_BF16 ? dispatch<bf16>(a, tab, st) : dispatch<float>(a, tab, st);
+    if (a.d.dtype != DTYPE_F32) return hipErrorInvalidValue;
+    if (a.d.dk == 128) return a.d.dv == 128 ? launch<128, 128>(a, tab, st) : launch<128, 64>(a, tab, st);
+    return a.d.dv == 128 ? launch<64, 128>(a, tab, st) : launch<64, 64>(a, tab, st);
 }
 
 hipError_t launch_gdn_sum_parts(const GdnBackwardArgs& a, hipStream_t st) {

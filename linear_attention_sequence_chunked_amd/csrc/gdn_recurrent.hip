@@ -37,7 +37,7 @@ struct RecArgs {
     float scale;
     void* out;
     // step form
-    int num_tokens, num_slots, num_seqs;
+    int num_tokens, num_slots;
     const int32_t *steps, *slots;
     float* state;
     bool update;
@@ -478,7 +478,7 @@ RecArgs common(const GdnDims& d) {
 hipError_t launch_gdn_recurrent(const GdnRecurrentArgs& a, hipStream_t stream) {
     RecArgs r = common(a.d);
     r.q = a.q; r.k = a.k; r.v = a.v; r.la = a.log_alpha; r.be = a.beta; r.out = a.out;
-    r.num_tokens = a.num_tokens; r.num_slots = a.num_slots; r.num_seqs = a.num_seqs;
+    r.num_tokens = a.num_tokens; r.num_slots = a.num_slots;
     r.steps = a.steps; r.slots = a.state_indices; r.state = a.state; r.update = a.update;
     const int64_t blocks = (int64_t)a.num_seqs * a.d.hv * (a.d.dv / a.nv);
     if (blocks == 0) return hipSuccess;
@@ -488,7 +488,7 @@ hipError_t launch_gdn_recurrent(const GdnRecurrentArgs& a, hipStream_t stream) {
         if (a.num_tokens == 1 && a.nv == DV)  // whole rows
             hipLaunchKernelGGL((decode_kernel<T, DK, DV, DV>), dim3((unsigned)blocks), dim3(kThreads), (whole_lds<DK, DV>()), stream, r);
         else if (a.num_tokens == 1)
-            hipLaunchKernelGGL((decode_kernel<T, DK, DV, NV>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, r);
+            hipLaunchKernelGGL((decode_kernel<T, DK, DV, 32>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, r);
         else if (a.num_tokens <= 4)
             hipLaunchKernelGGL((step_kernel<T, DK, DV, NV, 4>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, r);
         else
