@@ -20,7 +20,7 @@ SOURCES = ["kda_api.cpp", "kda_plan.cpp", "kda_decode.hip", "kda_prefill.hip", "
            "kda_spec.hip", "kda_segment.hip", "kda_backward.hip", "kda_scratch.hip",
            "gdn_api.cpp", "gdn_plan.cpp", "gdn_recurrent.hip", "gdn_prefill.hip", "gdn_backward.hip", "gdn_backward_seq.hip",
            "spec_accept.hip"]
-HEADERS = ["kda_device.h", "kda_launch.h", "kda_mfma.h", "kda_check.h", "gdn_launch.h", "gdn_chunk.h"]
+HEADERS = ["kda_device.h", "kda_launch.h", "kda_mfma.h", "kda_check.h", "gdn_launch.h", "gdn_chunk.h", "gdn_walk.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

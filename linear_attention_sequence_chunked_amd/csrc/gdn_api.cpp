@@ -74,8 +74,9 @@ kda_status check_grid(int64_t blocks, int64_t threads) {
 }
 
 // the (sequence, head) pairs of one launch, their columns cut finest, at most 1024 threads each
+// (704 and two walks in the gradients' first)
 kda_status check_pairs(const kda::GdnDims& d, int32_t num_seqs) {
-    return check_grid((int64_t)std::min(num_seqs, kda::kGdnSeqs) * d.hv * (d.dv / 16) + 64, 1024);
+    return check_grid(2 * ((int64_t)std::min(num_seqs, kda::kGdnSeqs) * d.hv * (d.dv / 16) + 64), 1024);
 }
 
 kda_status check_cu(const int32_t* cu, int32_t n) {
@@ -234,7 +235,7 @@ kda_status kda_gdn_prefill_backward(const kda_gdn_params* params, const void* q,
         const bool chunked = d.dtype == KDA_DTYPE_BF16;
         if (chunked) {
             a.states = ws + plan.off_a; a.sgrads = ws + plan.off_b; a.u = ws + plan.off_c; a.dx = ws + plan.off_d;
-            a.nv = kda::gdn_backward_nv(d.dv, (int64_t)num_seqs * d.hv, kda::device_cu_count());
+            a.cus = kda::device_cu_count();
         } else {
             a.checkpoints = reinterpret_cast<float*>(ws + plan.off_a);
             a.scratch = reinterpret_cast<float*>(ws + plan.off_b);

@@ -13,17 +13,19 @@
 //   dG_C = e^{G_C} <S, dS'> + sum_t e^{G_C - G} (U dS'^T)_t.k_t,
 //   dlog_alpha_t = dG_C + sum over the chunk's s >= t of dG_s.
 //
-// Three launches.  The forward walk (gdn_prefill.hip, SAVE) stores every chunk's S and U; the
-// walk below goes backwards over the chunks with dS in registers and stores dS' and dX; both
-// are latency-bound chains over slices of value columns, built alike.  The gradient kernel then
+// Two launches.  The first holds two walks, each a latency-bound chain over slices of value
+// columns: the forward one (gdn_walk.h, SAVE) stores every chunk's S and U, the one below goes
+// backwards over the chunks with dS in registers and stores dS' and dX.  Neither needs the
+// other's results, so they run side by side, workgroup by workgroup.  The gradient kernel then
 // takes every (chunk, value head) on its own: products over the value columns, then over the
 // chunk's tokens.
 //
 // Precision.  Gradients come at any scale, so their side cannot take fp16 operands: here the
 // computed operands are pairs of bf16 (16 bits, 4e-6 of a result's size in all; single ones
 // would leave the fp32 gradients 2e-3), q, k, v and dO single ones, which they are.
-#include "gdn_chunk.h"
-#include "gdn_launch.h"
+#include <algorithm>
+
+#include "gdn_walk.h"
 
 namespace kda {
 namespace {
@@ -38,7 +40,12 @@ __device__ __forceinline__ void pair8(f32x4 a, f32x4 b, bf16x8& hi, bf16x8& lo) 
 
 // ------------------------------------------------------------------------- the walk back
 
-template <int DK, int NCB>
+// Column blocks of 16 per workgroup, of both walks.  One block spreads few states over more
+// compute units but stages the keys as often: 2048 tokens, 4 heads of 128 x 128: 128 us with one,
+// 132 with two; 32 heads: 242 and 192.
+constexpr int NCB = 2;
+
+template <int DK>
 struct WCfg {
     static constexpr int KB = DK / 16, KP = DK / 32, NV = 16 * NCB;
     // wave numbers: chain (one per 16 columns), stage (4), inverse (2), gram (2)
@@ -64,25 +71,24 @@ struct WArgs {
     int64_t qs, ks;
     int hk, hv, dv, slices, groups;
     float scale;
-    GdnTable tab;
 };
 
 // Passes and phases as in the prefill's narrow form, the chunks in reverse order: pass c stages
 // chunk nch-1-c; the chain's phase A takes K dS' of the chunk staged a pass before, phase B the
 // rest of its step.  P^T is needed a phase earlier than there.
-template <int DK, int NCB>
-__global__ __launch_bounds__((WCfg<DK, NCB>::THREADS)) void gdn_walk_back_kernel(const WArgs a) {
-    typedef WCfg<DK, NCB> C;
+template <int DK>
+__device__ __forceinline__ void gdn_walk_back(const WArgs& a, const GdnTable& tab, int block) {
+    typedef WCfg<DK> C;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int kk = blockIdx.x >> 3;
-    const int group = (kk / a.slices) * 8 + (blockIdx.x & 7), slice = kk % a.slices;
+    const int kk = block >> 3;
+    const int group = (kk / a.slices) * 8 + (block & 7), slice = kk % a.slices;
     if (group >= a.groups) return;
     const int si = group / a.hv, h = group % a.hv, hk = h / (a.hv / a.hk);
-    const int len = a.tab.len[si], id = a.tab.id[si], col0 = slice * C::NV;
-    const int64_t start = a.tab.start[si];
+    const int len = tab.len[si], id = tab.id[si], col0 = slice * C::NV;
+    const int64_t start = tab.start[si];
     const int64_t sbase = ((int64_t)id * a.hv + h) * (int64_t)DK * a.dv;
     const int nch = (len + kGC - 1) / kGC;
     const int64_t slot0 = BwdSlot::index(start, id, len, a.hv, h, 0);
@@ -103,6 +109,13 @@ __global__ __launch_bounds__((WCfg<DK, NCB>::THREADS)) void gdn_walk_back_kernel
             lds_barrier();
         }
     };
+    if (wave >= C::W_GRAM + 2) {  // the forward walk has a wave more: this one keeps the barriers
+        for (int c = 0; c < passes; ++c) {
+            lds_barrier();
+            lds_barrier();
+        }
+        return;
+    }
     if (wave >= C::W_STAGE && wave < C::W_INV) {
         struct Staged {
             u32x4 k[C::K::PPT], q[C::K::PPT], o[C::V::PPT];
@@ -402,6 +415,25 @@ __global__ __launch_bounds__((WCfg<DK, NCB>::THREADS)) void gdn_walk_back_kernel
 #pragma unroll
             for (int i = 0; i < 4; ++i) a.dS0[sbase + (int64_t)(channel(b) + i) * a.dv + col] = D[b][i];
     }
+}
+
+// Both walks: stretches of workgroups, one per compute unit at most, first of the walk back (the
+// slower by a sixth), then of the forward one.  Four sequences of 4096 tokens with 16 heads fill
+// the card with each walk: 710 us in all, 743 with the walks' workgroups alternating, 711 as
+// launches of their own; 517 + 300 + 64 + 1 tokens with 4 heads of 64 x 128 leave it half empty:
+// 43 us, 63 as launches of their own.
+template <int DK>
+struct WalksCfg {
+    typedef GCfg<DK, NCB, true> F;
+    typedef WCfg<DK> B;
+    static constexpr int THREADS = F::THREADS, LDS_BYTES = F::LDS_BYTES > B::LDS_BYTES ? F::LDS_BYTES : B::LDS_BYTES;
+    static_assert(THREADS == B::THREADS + 64, "the walk back's spare wave");
+};
+template <int DK>
+__global__ __launch_bounds__((WalksCfg<DK>::THREADS)) void gdn_walks_kernel(const PArgs f, const WArgs b, const GdnTable tab, int stretch) {
+    const int s = blockIdx.x / stretch, block = (s >> 1) * stretch + blockIdx.x % stretch;
+    if (s & 1) gdn_walk<DK, NCB, true>(f, tab, block);
+    else gdn_walk_back<DK>(b, tab, block);
 }
 
 // ------------------------------------------------------------------------- the gradients
@@ -821,19 +853,24 @@ __global__ __launch_bounds__(256, 2) void gdn_gradients_kernel(const GdnBackward
     }
 }
 
-template <int DK, int NCB>
-hipError_t walk_back(const GdnBackwardArgs& p, const GdnTable& tab, hipStream_t st) {
-    typedef WCfg<DK, NCB> C;
+template <int DK>
+hipError_t walks(const GdnBackwardArgs& p, const GdnTable& tab, hipStream_t st) {
+    typedef WalksCfg<DK> C;
+    GdnPrefillArgs f = {};
+    f.d = p.d; f.num_seqs = p.num_seqs; f.q = p.q; f.k = p.k; f.v = p.v; f.log_alpha = p.log_alpha; f.beta = p.beta;
+    f.initial_state = p.initial_state; f.nv = 16 * NCB;
+    PArgs fa = walk_args(f);
+    fa.save_s = (bf16*)p.states; fa.save_u = (bf16*)p.u;
     WArgs a;
     a.q = (const bf16*)p.q; a.k = (const bf16*)p.k; a.d_out = (const bf16*)p.d_out; a.la = p.log_alpha; a.be = p.beta;
     a.dSf = p.d_final_state; a.dS0 = p.d_initial_state; a.sgrads = (bf16*)p.sgrads; a.dx = (bf16*)p.dx;
-    a.qs = p.d.qs; a.ks = p.d.ks; a.hk = p.d.hk; a.hv = p.d.hv; a.dv = p.d.dv; a.slices = p.d.dv / C::NV;
-    a.groups = p.num_seqs * p.d.hv; a.scale = p.d.scale; a.tab = tab;
-    const int64_t blocks = ((int64_t)a.groups + 7) / 8 * 8 * a.slices;
-    hipError_t e = hipFuncSetAttribute((const void*)gdn_walk_back_kernel<DK, NCB>, hipFuncAttributeMaxDynamicSharedMemorySize,
+    a.qs = p.d.qs; a.ks = p.d.ks; a.hk = p.d.hk; a.hv = p.d.hv; a.dv = p.d.dv; a.slices = fa.slices; a.groups = fa.groups;
+    a.scale = p.d.scale;
+    hipError_t e = hipFuncSetAttribute((const void*)gdn_walks_kernel<DK>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                        C::LDS_BYTES);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gdn_walk_back_kernel<DK, NCB>), dim3((unsigned)blocks), dim3(C::THREADS), C::LDS_BYTES, st, a);
+    const int64_t blocks = walk_blocks(f), stretch = std::min<int64_t>(blocks, p.cus), grid = (blocks + stretch - 1) / stretch * 2 * stretch;
+    hipLaunchKernelGGL((gdn_walks_kernel<DK>), dim3((unsigned)grid), dim3(C::THREADS), C::LDS_BYTES, st, fa, a, tab, (int)stretch);
     return hipGetLastError();
 }
 
@@ -858,13 +895,7 @@ hipError_t gradients(const GdnBackwardArgs& p, const GdnTable& tab, hipStream_t 
 }  // namespace
 
 hipError_t launch_gdn_backward_chunked(const GdnBackwardArgs& p, const GdnTable& tab, hipStream_t st) {
-    GdnPrefillArgs f = {};
-    f.d = p.d; f.num_seqs = p.num_seqs; f.q = p.q; f.k = p.k; f.v = p.v; f.log_alpha = p.log_alpha; f.beta = p.beta;
-    f.initial_state = p.initial_state; f.nv = p.nv; f.save_states = p.states; f.save_u = p.u;
-    hipError_t e = launch_gdn_chunked(f, tab, st);
-    if (e != hipSuccess) return e;
-    if (p.d.dk == 128) e = p.nv == 16 ? walk_back<128, 1>(p, tab, st) : walk_back<128, 2>(p, tab, st);
-    else e = p.nv == 16 ? walk_back<64, 1>(p, tab, st) : walk_back<64, 2>(p, tab, st);
+    const hipError_t e = p.d.dk == 128 ? walks<128>(p, tab, st) : walks<64>(p, tab, st);
     if (e != hipSuccess) return e;
     if (p.d.dk == 128) return p.d.dv == 128 ? gradients<128, 128>(p, tab, st) : gradients<128, 64>(p, tab, st);
     return p.d.dv == 128 ? gradients<64, 128>(p, tab, st) : gradients<64, 64>(p, tab, st);

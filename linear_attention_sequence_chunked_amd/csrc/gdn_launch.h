@@ -33,8 +33,6 @@ struct GdnPrefillArgs {
     float* final_state;          // may be null
     void* out;
     int nv;                      // value columns per workgroup
-    // the backward's states: each chunk's S and U as bf16 pairs, no outputs (both or neither)
-    void *save_states, *save_u;
 };
 
 constexpr int kGdnMaxTokens = 16;  // tokens per sequence of the recurrent form
@@ -69,7 +67,7 @@ struct GdnBackwardArgs {
     int slots;                    // workgroups the scratch serves
     // in chunks: per (chunk, value head) the states, their gradients, U and dX (gdn_chunk.h)
     void *states, *sgrads, *u, *dx;
-    int nv;
+    int cus;  // compute units of the device
 };
 
 struct AcceptArgs {
@@ -89,8 +87,6 @@ struct AcceptArgs {
 int gdn_recurrent_nv(int dv, int64_t pairs, int tokens, int cu_count);
 // value columns per workgroup of the chunked prefill (gdn_plan.cpp)
 int gdn_prefill_nv(int dv, int64_t pairs, int cu_count);
-// value columns per workgroup of the backward's walks (gdn_plan.cpp)
-int gdn_backward_nv(int dv, int64_t pairs, int cu_count);
 // sequences from place `from` of a table (longest first) on that share a launch of the chunks'
 // gradients; 0: none of them has a token (gdn_plan.cpp)
 int gdn_gradient_group(const GdnTable& t, int from, int n, int hv);

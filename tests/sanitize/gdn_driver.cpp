@@ -29,7 +29,7 @@ hipError_t launch_gdn_backward_seq(const GdnBackwardArgs& a, const GdnTable& t, 
 }
 hipError_t launch_gdn_backward_chunked(const GdnBackwardArgs& a, const GdnTable& t, hipStream_t) {
     for (int i = 0; i < a.num_seqs; ++i) g_tokens += t.len[i];
-    return a.nv == 16 || a.nv == 32 ? hipSuccess : hipErrorInvalidValue;
+    return a.cus > 0 ? hipSuccess : hipErrorInvalidValue;
 }
 hipError_t launch_gdn_sum_parts(const GdnBackwardArgs& a, hipStream_t) { return a.parts ? hipSuccess : hipErrorInvalidValue; }
 hipError_t launch_accept(const AcceptArgs& a, hipStream_t) {
