@@ -82,24 +82,7 @@ __device__ __forceinline__ void store_key(unsigned char* tile, const u32x4 (&src
     }
 }
 
-// The decays of a chunk, all in units of log2: lane t of one wave holds token t.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double dpp_f64(double x) {
-    const uint64_t w = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)w, CTRL, ROWS, 0xF, true);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(w >> 32), CTRL, ROWS, 0xF, true);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double wave_scan_f64(double x) {
-    x += dpp_f64<0x111, 0xF>(x);  // within rows of 16
-    x += dpp_f64<0x112, 0xF>(x);
-    x += dpp_f64<0x114, 0xF>(x);
-    x += dpp_f64<0x118, 0xF>(x);
-    x += dpp_f64<0x142, 0xA>(x);  // lane 15 -> row 1, 47 -> row 3
-    x += dpp_f64<0x143, 0xC>(x);  // lane 31 -> rows 2, 3
-    return x;
-}
-// A log-decay below -1000 (its factor is 0 in any case) is taken as -1000, so that sums behind
+// The decays of a chunk, all in units of log2: lane t of one wave holds token t.  A log-decay below -1000 (its factor is 0 in any case) is taken as -1000, so that sums behind
 // it keep their accuracy and -inf - -inf does not arise; NaN stays.
 __device__ __forceinline__ double log2_decay(float la) { return (la < -1000.f ? -1000.0 : (double)la) * 1.4426950408889634074; }
 

@@ -90,6 +90,9 @@ int gdn_prefill_nv(int dv, int64_t pairs, int cu_count);
 // sequences from place `from` of a table (longest first) on that share a launch of the chunks'
 // gradients; 0: none of them has a token (gdn_plan.cpp)
 int gdn_gradient_group(const GdnTable& t, int from, int n, int hv);
+// vocabulary that one workgroup holds in registers, and whether this one does (gdn_plan.cpp)
+constexpr int64_t kAcceptOne = 32768;
+bool accept_in_one(int64_t vocab);
 // pieces the vocabulary of one sequence is cut into (gdn_plan.cpp)
 int accept_pieces(int64_t num_seqs, int64_t vocab, int cu_count);
 

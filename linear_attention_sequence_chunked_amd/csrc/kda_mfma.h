@@ -129,6 +129,24 @@ __device__ __forceinline__ void row_scan8(float (&x)[8]) {
     for (int j = 0; j < 8; ++j) x[j] += dpp<0x118>(x[j]);
 }
 
+// inclusive prefix sum over the 64 lanes in fp64
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double x) {
+    const uint64_t w = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)w, CTRL, ROWS, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(w >> 32), CTRL, ROWS, 0xF, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_scan_f64(double x) {
+    x += dpp_f64<0x111, 0xF>(x);  // within rows of 16
+    x += dpp_f64<0x112, 0xF>(x);
+    x += dpp_f64<0x114, 0xF>(x);
+    x += dpp_f64<0x118, 0xF>(x);
+    x += dpp_f64<0x142, 0xA>(x);  // lane 15 -> row 1, 47 -> row 3
+    x += dpp_f64<0x143, 0xC>(x);  // lane 31 -> rows 2, 3
+    return x;
+}
+
 // Workgroup barrier that orders LDS only.  __syncthreads() also waits for every
 // outstanding global load, which would drain the multi-chunk prefetch at each chunk.
 __device__ __forceinline__ void lds_barrier() {

@@ -15,10 +15,11 @@
 // vocabulary is cut into pieces, so that one sequence also spreads over the card: a first
 // launch finds the kept drafts and sums each piece, a second finds the piece that holds the
 // draw from the sums (in piece order: the same result whatever ran first) and scans that piece
-// alone.
+// alone.  A vocabulary that fits one workgroup's registers takes one launch instead.
 #include "gdn_launch.h"
 #include "kda_device.h"
 #include "kda_launch.h"
+#include "kda_mfma.h"
 
 namespace kda {
 namespace {
@@ -172,11 +173,7 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(const AcceptArgs A) {
 // inclusive scan over the workgroup's 256 values; total in `all`
 __device__ double scan(double x, double* s_wave, double& all) {
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double y = __shfl_up(x, off);
-        if (lane >= off) x += y;
-    }
+    x = wave_scan_f64(x);
     __syncthreads();
     if (lane == 63) s_wave[wave] = x;
     __syncthreads();
@@ -280,8 +277,137 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(const AcceptArgs A) {
             j < R.kept ? A.tokens[(int64_t)n * A.num_draft + j] : (j == R.kept ? (int32_t)drawn : -1);
 }
 
+// The whole of it in one workgroup per sequence, its two rows in registers: thread t holds
+// entries N (1024 j + t) .. +N-1 of every round j, so the order of the vocabulary is that of
+// (round, wave, lane).  A segment is a round's share of a wave; the segment of the draw is found
+// from all segments' sums by every wave, the entry by the segment's own.
+constexpr int kOneThreads = 1024;
+template <typename T>
+__global__ __launch_bounds__(kOneThreads) void one_kernel(const AcceptArgs A) {
+    constexpr int N = Packed<T>::N, ROUNDS = (int)(kAcceptOne / (kOneThreads * N)), WAVES = kOneThreads / 64, SEG = WAVES * ROUNDS,
+                  PL = SEG / 64;
+    static_assert(PL * 64 == SEG, "whole lanes of segments");
+    __shared__ double s_seg[2][SEG];
+    const int n = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    Row R;
+    R.kept = count_kept<T>(A, n, lane, &R.rejected);  // (every wave: no wait for another's)
+    const T *p, *q;
+    int64_t certain;
+    row_of(A, n, R, p, q, certain);
+    // entries behind the row's end: the last N are loaded again, and weigh nothing where they
+    // lie before the thread's own
+    const int vocab = (int)A.vocab;
+    auto own = [&](int j) { return N * (kOneThreads * j + t); };
+    auto from = [&](int j) { return min(own(j), vocab - N); };
+    u32x4 a[ROUNDS], b[ROUNDS] = {};
+    auto load = [](const T* x) { return __builtin_bit_cast(u32x4, *reinterpret_cast<const Packed<T>*>(x)); };
+#pragma unroll
+    for (int j = 0; j < ROUNDS; ++j) a[j] = load(p + from(j));
+    if (q) {
+#pragma unroll
+        for (int j = 0; j < ROUNDS; ++j) b[j] = load(q + from(j));
+    }
+    const double u = (double)A.uniforms[(int64_t)n * (A.num_draft + 1) + A.num_draft];
+    int32_t* out = A.out + (int64_t)n * (A.num_draft + 1);
+    if (t == 0) A.accepted[n] = R.kept;
+    if (t <= A.num_draft && t != R.kept) out[t] = t < R.kept ? A.tokens[(int64_t)n * A.num_draft + t] : -1;
+    auto first_of = [](unsigned long long m) { return (int)__builtin_ctzll(m); };
+    auto last_of = [](unsigned long long m) { return 63 - (int)__builtin_clzll(m); };
+    // first the draw's weights, then (nothing left of them) p's
+#pragma unroll 1
+    for (int plain = 0; plain < 2; ++plain) {
+        // (opaque, or the compiler keeps every entry's fp64 forms across the loop: twice the registers)
+#pragma unroll
+        for (int j = 0; j < ROUNDS; ++j) asm volatile("" : "+v"(a[j]), "+v"(b[j]));
+        auto weight = [&](u32x4 pw, u32x4 qw, int j, int e) {
+            const Packed<T> pe = __builtin_bit_cast(Packed<T>, pw), qe = __builtin_bit_cast(Packed<T>, qw);
+            const double pv = to_f32(pe.v[e]);
+            double w = pv > 0.0 ? pv : 0.0;
+            if (!plain) {
+                if (q) {
+                    const double d = pv - (double)to_f32(qe.v[e]);
+                    w = d > 0.0 ? d : 0.0;  // NaN counts as nothing
+                }
+                if (from(j) + e == certain) w = 0.0;
+            }
+            return from(j) + e >= own(j) ? w : 0.0;
+        };
+#pragma unroll
+        for (int j = 0; j < ROUNDS; ++j) {
+            double sum = 0.0;
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum += weight(a[j], b[j], j, e);
+            sum = wave_scan_f64(sum);
+            if (lane == 63) s_seg[plain][WAVES * j + wave] = sum;
+            __builtin_amdgcn_sched_barrier(0);  // (one round's fp64 at a time in registers)
+        }
+        __syncthreads();
+        double x[PL], mine = 0.0;
+#pragma unroll
+        for (int e = 0; e < PL; ++e) {
+            x[e] = s_seg[plain][PL * lane + e];
+            mine += x[e];
+        }
+        const double after = wave_scan_f64(mine), all = __shfl(after, 63);
+        if (!(all > 0.0)) continue;  // (the same in every wave)
+        const double target = u * all;
+        double c = after - mine, before = 0.0;
+        int first = -1, last = -1;
+#pragma unroll
+        for (int e = 0; e < PL; ++e) {
+            if (x[e] > 0.0) {
+                if (first < 0 && c + x[e] > target) {
+                    first = PL * lane + e;
+                    before = c;
+                }
+                last = PL * lane + e;
+            }
+            c += x[e];
+        }
+        const unsigned long long hit = __ballot(first >= 0);
+        // u * total not below any sum: the last entry
+        const int src = hit ? first_of(hit) : last_of(__ballot(last >= 0));
+        const int seg = __builtin_amdgcn_readfirstlane(__shfl(hit ? first : last, src));
+        before = __shfl(before, src);
+        if (seg % WAVES != wave) return;
+        const int round = seg / WAVES;
+        u32x4 pe = a[0], qe = b[0];
+#pragma unroll
+        for (int j = 1; j < ROUNDS; ++j)
+            if (j == round) {
+                pe = a[j];
+                qe = b[j];
+            }
+        double w[N], sum = 0.0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            w[e] = weight(pe, qe, round, e);
+            sum += w[e];
+        }
+        double s = before + (wave_scan_f64(sum) - sum);
+        int at = -1, end = -1;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            s += w[e];
+            if (w[e] > 0.0) {
+                if (hit && at < 0 && s > target) at = from(round) + e;
+                end = from(round) + e;
+            }
+        }
+        const unsigned long long inside = __ballot(at >= 0);
+        const int who = inside ? first_of(inside) : last_of(__ballot(end >= 0));
+        if (lane == who) out[R.kept] = inside ? at : end;
+        return;
+    }
+    if (t == 0) out[R.kept] = -1;  // no entry has any weight
+}
+
 template <typename T>
 hipError_t launch_typed(const AcceptArgs& a, hipStream_t stream) {
+    if (accept_in_one(a.vocab)) {
+        hipLaunchKernelGGL((one_kernel<T>), dim3((unsigned)a.num_seqs), dim3(kOneThreads), 0, stream, a);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL((sum_kernel<T>), dim3((unsigned)(a.num_seqs * (int64_t)a.pieces)), dim3(kThreads), 0,
                        stream, a);
     hipError_t e = hipGetLastError();

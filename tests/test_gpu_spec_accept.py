@@ -37,6 +37,27 @@ def test_accept_sizes(dtype, N, K, V):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [7, 8, 9, 15, 511, 4095, 4096, 4100, 8193, 16385, 32767, 32768, 32769])
+def test_accept_vocabularies_around_one_workgroups(V, dtype):
+    """Rows of one round and several, up to the registers of one workgroup and past them."""
+    check(*case(7, 3, V, dtype, seed=V))
+
+
+@pytest.mark.parametrize("V", [9, 4099, 32768, 40000])
+def test_accept_draws_at_the_ends(V):
+    """The draw's border below the first entry and above the last, rows with a single entry."""
+    p, q, x, u = case(12, 1, V, "f32", seed=V + 1)
+    u[:, 0] = 0.999
+    q[:, 0] = 0.0
+    q.scatter_(2, x[:, :, None].long(), 1e6)  # the draft is rejected, its own entry weighs nothing
+    u[:4, 1], u[4:8, 1], u[8:, 1] = 0.0, 1.0 - 2.0 ** -24, 0.5
+    for n in range(8, 12):
+        p[n] = 0.0
+        p[n, 0, [0, V - 1, V // 2, (V - 1) // 64 * 64][n - 8]] = 0.25
+    check(p, q, x, u)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_accept_ragged_counts(dtype):
     p, q, x, u = case(12, 5, 1003, dtype, seed=2)
     counts = torch.tensor([0, 1, 2, 3, 4, 5, 0, -2, 9, 5, 1, 2], dtype=torch.int32, device="cuda")
