@@ -56,11 +56,17 @@ def _head_dims(q, v):
 
 def _params(q, k, v, scale):
     hk, hv, dk, dv = _head_dims(q, v)
-    dt, dev, lead = q.dtype, q.device, q.shape[:-2]
-    if k.shape[:-2] != lead or v.shape[:-2] != lead:
-        raise ValueError(f"q, k and v must lead with {tuple(lead)}: {tuple(k.shape)}, {tuple(v.shape)}")
-    return _lib.GdnParams(_DT[dt], hk, hv, dk, dv, scale, _tokens("q", q, hk, dk, dt, dev),
-                          _tokens("k", k, hk, dk, dt, dev), _tokens("v", v, hv, dv, dt, dev))
+    dt, dev, qs, vs = q.dtype, q.device, q.shape, v.shape
+    if k.shape != qs or vs[:-2] != qs[:-2]:
+        raise ValueError(f"k must have q's shape {tuple(qs)} and v lead like it: {tuple(k.shape)}, {tuple(vs)}")
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != dt or t.device != dev:
+            raise ValueError(f"{name} is {t.dtype} on {t.device}, q {dt} on {dev}")
+    # (0: dense)
+    return _lib.GdnParams(_DT[dt], hk, hv, dk, dv, scale,
+                          0 if q.is_contiguous() else _tokens("q", q, hk, dk, dt, dev),
+                          0 if k.is_contiguous() else _tokens("k", k, hk, dk, dt, dev),
+                          0 if v.is_contiguous() else _tokens("v", v, hv, dv, dt, dev))
 
 
 # The current stream's handle; the public way makes a Stream object for it (1.9 us against 0.1,
