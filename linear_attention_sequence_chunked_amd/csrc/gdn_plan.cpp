@@ -48,9 +48,10 @@ int gdn_gradient_group(const GdnTable& t, int from, int n, int hv) {
 }
 
 bool accept_in_one(int64_t vocab) {
-    // One workgroup per sequence, one launch: 32000 entries of fp32, 1 / 128 / 512 sequences 9.1 /
-    // 10.2 / 27 us, against 14.3 / 20.3 / 38 with the vocabulary in pieces and a second launch
-    // (512 x 2000: 17.9 and 16.0).  At least the eight entries of a bf16 load.
+    // One workgroup per sequence, one launch, against the vocabulary in pieces and a second launch
+    // (fp32, replayed from a graph): 32000 entries, 1 / 128 / 512 sequences 8.8 / 10.2 / 27 us and
+    // 8.2 / 13.7 / 31; 500 entries, one sequence 3.5 and 6.5; called from the host one by one 10.0
+    // and 12.0.  At least the eight entries of a bf16 load.
     return vocab >= 8 && vocab <= kAcceptOne;
 }
 

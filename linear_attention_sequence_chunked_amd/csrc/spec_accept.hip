@@ -11,11 +11,14 @@
 // are fp64: the products and differences of fp32 values are exact there, and a draw is
 // decided by where a sum over the whole vocabulary crosses a border.
 //
-// Bound by reading one row of p and one of q per sequence; everything else is latency.  The
-// vocabulary is cut into pieces, so that one sequence also spreads over the card: a first
-// launch finds the kept drafts and sums each piece, a second finds the piece that holds the
-// draw from the sums (in piece order: the same result whatever ran first) and scans that piece
-// alone.  A vocabulary that fits one workgroup's registers takes one launch instead.
+// Bound by reading one row of p and one of q per sequence; everything else is latency.  A row
+// that fits the registers of one workgroup takes one launch (32000 entries of fp32: 8.8 us for one
+// sequence, about two of them the launch itself and the rest three dependent loads and the row).
+// Longer vocabularies are cut into pieces, so that one sequence also spreads over the card: a
+// first launch finds the kept drafts and sums each piece (128 sequences of 151669 entries, 155 MB:
+// 23.6 us, 6.6 TB/s with part of it in the last-level cache), a second finds the piece that holds
+// the draw from the sums (in piece order: the same result whatever ran first) and scans that piece
+// alone (5.1 us; 13.9 with four waves, scans through LDS and atomic minima).
 #include "gdn_launch.h"
 #include "kda_device.h"
 #include "kda_launch.h"
@@ -170,123 +173,147 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(const AcceptArgs A) {
             (s_sum[0][threadIdx.x] + s_sum[1][threadIdx.x]) + (s_sum[2][threadIdx.x] + s_sum[3][threadIdx.x]);
 }
 
-// inclusive scan over the workgroup's 256 values; total in `all`
-__device__ double scan(double x, double* s_wave, double& all) {
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    x = wave_scan_f64(x);
-    __syncthreads();
-    if (lane == 63) s_wave[wave] = x;
-    __syncthreads();
-    double before = 0.0;
-    for (int w = 0; w < wave; ++w) before += s_wave[w];
-    all = ((s_wave[0] + s_wave[1]) + s_wave[2]) + s_wave[3];
-    return before + x;
+constexpr int kOneThreads = 1024;  // of the launches that draw
+
+__device__ inline int first_of(unsigned long long m) { return (int)__builtin_ctzll(m); }
+__device__ inline int last_of(unsigned long long m) { return 63 - (int)__builtin_clzll(m); }
+
+// Where the running sum of PL values per lane (x, in lane order, behind `before`) first exceeds
+// `target`: that value's place, and the sum in front of it; with none, the last value above 0 and
+// found = false.  Every lane returns the same.
+template <int PL>
+__device__ inline int crossing(const double (&x)[PL], double before, double target, int lane, double& front, bool& found) {
+    double mine = 0.0;
+#pragma unroll
+    for (int e = 0; e < PL; ++e) mine += x[e];
+    double c = before + (wave_scan_f64(mine) - mine), at = 0.0;
+    int first = -1, last = -1;
+#pragma unroll
+    for (int e = 0; e < PL; ++e) {
+        if (x[e] > 0.0) {
+            if (first < 0 && c + x[e] > target) {
+                first = PL * lane + e;
+                at = c;
+            }
+            last = PL * lane + e;
+        }
+        c += x[e];
+    }
+    const unsigned long long hit = __ballot(first >= 0), any = __ballot(last >= 0);
+    found = hit != 0;
+    if (!any) return -1;
+    const int src = hit ? first_of(hit) : last_of(any);
+    front = __shfl(at, src);
+    return __builtin_amdgcn_readfirstlane(__shfl(hit ? first : last, src));
 }
 
-// sixteen consecutive entries per thread are weighed in registers, kept across the scan
+// The second launch: the piece of the draw from the pieces' sums (every wave by itself), then its
+// entry, a round of N per thread at a time (a piece is one round, but of vocabularies above 2^20).
 template <typename T>
-__global__ __launch_bounds__(kThreads) void draw_kernel(const AcceptArgs A) {
-    constexpr int N = Packed<T>::N, PER = 16;
-    __shared__ double s_wave[4];
-    __shared__ double s_before;
-    __shared__ int s_piece, s_last;
-    __shared__ long long s_at, s_end;
-    const int n = blockIdx.x, t = threadIdx.x;
+__global__ __launch_bounds__(kOneThreads) void draw_kernel(const AcceptArgs A) {
+    constexpr int N = Packed<T>::N, WAVES = kOneThreads / 64, PL = 4;
+    __shared__ double s_seg[2][WAVES];
+    __shared__ int s_end;
+    const int n = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     Row R;
     R.kept = A.accepted[n];  // the first launch's
     R.rejected = R.kept < (A.num_drafts ? min(max(A.num_drafts[n], 0), A.num_draft) : A.num_draft);
     const T *p, *q;
     int64_t certain;
     row_of(A, n, R, p, q, certain);
-    if (t == 0) {
-        s_piece = A.pieces;
-        s_last = -1;
-        s_at = A.vocab;
-        s_end = -1;
+    double x[PL], xp[PL], mine = 0.0, mine_p = 0.0;
+#pragma unroll
+    for (int e = 0; e < PL; ++e) {
+        const int piece = PL * lane + e;
+        const bool in = piece < A.pieces;
+        x[e] = in ? A.partial[2 * ((int64_t)n * A.pieces + piece)] : 0.0;
+        xp[e] = in ? A.partial[2 * ((int64_t)n * A.pieces + piece) + 1] : 0.0;
+        mine += x[e];
+        mine_p += xp[e];
     }
-    // the piece that holds the draw: the first whose inclusive sum exceeds u * total
-    const double mine_r = t < A.pieces ? A.partial[2 * ((int64_t)n * A.pieces + t)] : 0.0;
-    const double mine_p = t < A.pieces ? A.partial[2 * ((int64_t)n * A.pieces + t) + 1] : 0.0;
     const double u = (double)A.uniforms[(int64_t)n * (A.num_draft + 1) + A.num_draft];
-    double mine = mine_r, all;
-    double inc = scan(mine, s_wave, all);
+    int32_t* out = A.out + (int64_t)n * (A.num_draft + 1);
+    if (t <= A.num_draft && t != R.kept) out[t] = t < R.kept ? A.tokens[(int64_t)n * A.num_draft + t] : -1;
+    if (t == 0) s_end = -1;
+    double all = __shfl(wave_scan_f64(mine), 63);
     const bool plain = !(all > 0.0);  // nothing left: draw from p
     if (plain) {
-        mine = mine_p;
-        inc = scan(mine, s_wave, all);
+        all = __shfl(wave_scan_f64(mine_p), 63);
+#pragma unroll
+        for (int e = 0; e < PL; ++e) x[e] = xp[e];
     }
     const double target = u * all;
-    if (mine > 0.0) {
-        if (inc > target) atomicMin(&s_piece, t);
-        atomicMax(&s_last, t);
+    double before;
+    bool inside;
+    const int piece = crossing<PL>(x, 0.0, target, lane, before, inside);
+    if (piece < 0) {  // no entry has any weight
+        if (t == 0) out[R.kept] = -1;
+        return;
     }
-    __syncthreads();
-    const bool inside = s_piece < A.pieces;
-    const int piece = inside ? s_piece : s_last;  // u * total not below any sum: the last entry
-    if (t == piece) s_before = inside ? inc - mine : 0.0;
-    __syncthreads();
-    int64_t drawn = -1;
-    if (piece >= 0) {  // -1: no entry has any weight
-        const int64_t lo = piece * A.piece, hi = min(lo + A.piece, A.vocab);
-        double before = s_before;
-        for (int64_t at = lo; at < hi; at += PER * kThreads) {
-            const int64_t i0 = at + PER * t;
-            double w[PER], sum = 0.0;
-#pragma unroll
-            for (int k = 0; k < PER / N; ++k) {
-                const int64_t i = i0 + N * k;
-                double r[N] = {}, pp[N] = {};
-                if (i + N <= hi) {
-                    weights16(p, q, i, certain, r, pp);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        if (i + j < hi) {
-                            const Weights x = weights(p, q, i + j, certain);
-                            r[j] = x.r;
-                            pp[j] = x.p;
-                        }
-                }
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    w[N * k + j] = plain ? pp[j] : r[j];
-                    sum += w[N * k + j];
-                }
+    const int64_t lo = piece * A.piece, hi = min(lo + A.piece, A.vocab);
+    int turn = 0;
+    int64_t last = -1;
+    for (int64_t at = lo; at < hi; at += N * kOneThreads) {
+        // (entries behind the piece's end: the row's last N again, weighing nothing)
+        const int64_t own = at + N * t, from = min(own, A.vocab - N);
+        double w[N], sum = 0.0, r[N] = {}, pp[N] = {};
+        if (A.vocab >= N) {
+            weights16(p, q, from, certain, r, pp);
+        } else if (t == 0) {
+            for (int e = 0; e < (int)A.vocab; ++e) {
+                const Weights y = weights(p, q, e, certain);
+                r[e - (int)from] = y.r;
+                pp[e - (int)from] = y.p;
             }
-            double local_all;
-            double c = before + scan(sum, s_wave, local_all) - sum;
-            int64_t first = A.vocab, last = -1;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                c += w[j];
-                if (w[j] > 0.0) {
-                    if (c > target && first == A.vocab) first = i0 + j;
-                    last = i0 + j;
-                }
-            }
-            if (first < A.vocab) atomicMin(&s_at, (long long)first);
-            if (last >= 0) atomicMax(&s_end, (long long)last);
-            before += local_all;
-            __syncthreads();
-            if (inside && s_at < A.vocab) break;
         }
-        drawn = (inside && s_at < A.vocab) ? s_at : s_end;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            w[e] = from + e >= own && from + e < hi ? (plain ? pp[e] : r[e]) : 0.0;
+            sum += w[e];
+        }
+        const double inc = wave_scan_f64(sum);
+        if (lane == 63) s_seg[turn][wave] = inc;
+        __syncthreads();
+        const double seg[1] = {lane < WAVES ? s_seg[turn][lane] : 0.0};
+        turn ^= 1;
+        double front;
+        bool found;
+        const int s = crossing<1>(seg, before, inside ? target : __builtin_inf(), lane, front, found);
+        if (found) {
+            if (s != wave) return;
+            double c = front + (inc - sum);
+            int first = -1, end = -1;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                c += w[e];
+                if (w[e] > 0.0) {
+                    if (first < 0 && c > target) first = (int)(from + e);
+                    end = (int)(from + e);
+                }
+            }
+            const unsigned long long hit = __ballot(first >= 0);
+            const int who = hit ? first_of(hit) : last_of(__ballot(end >= 0));
+            if (lane == who) out[R.kept] = hit ? first : end;
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (w[e] > 0.0) last = from + e;
+        before += __shfl(wave_scan_f64(seg[0]), 63);
     }
-    for (int j = t; j <= A.num_draft; j += kThreads)
-        A.out[(int64_t)n * (A.num_draft + 1) + j] =
-            j < R.kept ? A.tokens[(int64_t)n * A.num_draft + j] : (j == R.kept ? (int32_t)drawn : -1);
+    // u * total not below any sum: the piece's last entry
+    if (last >= 0) atomicMax(&s_end, (int)last);
+    __syncthreads();
+    if (t == 0) out[R.kept] = s_end;
 }
 
 // The whole of it in one workgroup per sequence, its two rows in registers: thread t holds
 // entries N (1024 j + t) .. +N-1 of every round j, so the order of the vocabulary is that of
 // (round, wave, lane).  A segment is a round's share of a wave; the segment of the draw is found
 // from all segments' sums by every wave, the entry by the segment's own.
-constexpr int kOneThreads = 1024;
-template <typename T>
+template <typename T, int ROUNDS>
 __global__ __launch_bounds__(kOneThreads) void one_kernel(const AcceptArgs A) {
-    constexpr int N = Packed<T>::N, ROUNDS = (int)(kAcceptOne / (kOneThreads * N)), WAVES = kOneThreads / 64, SEG = WAVES * ROUNDS,
-                  PL = SEG / 64;
-    static_assert(PL * 64 == SEG, "whole lanes of segments");
+    constexpr int N = Packed<T>::N, WAVES = kOneThreads / 64, SEG = WAVES * ROUNDS, PL = (SEG + 63) / 64;
     __shared__ double s_seg[2][SEG];
     const int n = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     Row R;
@@ -311,8 +338,6 @@ __global__ __launch_bounds__(kOneThreads) void one_kernel(const AcceptArgs A) {
     int32_t* out = A.out + (int64_t)n * (A.num_draft + 1);
     if (t == 0) A.accepted[n] = R.kept;
     if (t <= A.num_draft && t != R.kept) out[t] = t < R.kept ? A.tokens[(int64_t)n * A.num_draft + t] : -1;
-    auto first_of = [](unsigned long long m) { return (int)__builtin_ctzll(m); };
-    auto last_of = [](unsigned long long m) { return 63 - (int)__builtin_clzll(m); };
     // first the draw's weights, then (nothing left of them) p's
 #pragma unroll 1
     for (int plain = 0; plain < 2; ++plain) {
@@ -345,30 +370,15 @@ __global__ __launch_bounds__(kOneThreads) void one_kernel(const AcceptArgs A) {
         double x[PL], mine = 0.0;
 #pragma unroll
         for (int e = 0; e < PL; ++e) {
-            x[e] = s_seg[plain][PL * lane + e];
+            x[e] = PL * lane + e < SEG ? s_seg[plain][PL * lane + e] : 0.0;
             mine += x[e];
         }
-        const double after = wave_scan_f64(mine), all = __shfl(after, 63);
+        const double all = __shfl(wave_scan_f64(mine), 63);
         if (!(all > 0.0)) continue;  // (the same in every wave)
         const double target = u * all;
-        double c = after - mine, before = 0.0;
-        int first = -1, last = -1;
-#pragma unroll
-        for (int e = 0; e < PL; ++e) {
-            if (x[e] > 0.0) {
-                if (first < 0 && c + x[e] > target) {
-                    first = PL * lane + e;
-                    before = c;
-                }
-                last = PL * lane + e;
-            }
-            c += x[e];
-        }
-        const unsigned long long hit = __ballot(first >= 0);
-        // u * total not below any sum: the last entry
-        const int src = hit ? first_of(hit) : last_of(__ballot(last >= 0));
-        const int seg = __builtin_amdgcn_readfirstlane(__shfl(hit ? first : last, src));
-        before = __shfl(before, src);
+        double before;
+        bool hit;
+        const int seg = crossing<PL>(x, 0.0, target, lane, before, hit);
         if (seg % WAVES != wave) return;
         const int round = seg / WAVES;
         u32x4 pe = a[0], qe = b[0];
@@ -405,14 +415,21 @@ __global__ __launch_bounds__(kOneThreads) void one_kernel(const AcceptArgs A) {
 template <typename T>
 hipError_t launch_typed(const AcceptArgs& a, hipStream_t stream) {
     if (accept_in_one(a.vocab)) {
-        hipLaunchKernelGGL((one_kernel<T>), dim3((unsigned)a.num_seqs), dim3(kOneThreads), 0, stream, a);
+        // the fewest rounds (a power of two) that hold a row
+        constexpr int64_t round = kOneThreads * Packed<T>::N;
+        const dim3 grid((unsigned)a.num_seqs), block(kOneThreads);
+        if (a.vocab <= round) hipLaunchKernelGGL((one_kernel<T, 1>), grid, block, 0, stream, a);
+        else if (a.vocab <= 2 * round) hipLaunchKernelGGL((one_kernel<T, 2>), grid, block, 0, stream, a);
+        else if (a.vocab <= 4 * round) hipLaunchKernelGGL((one_kernel<T, 4>), grid, block, 0, stream, a);
+        else if constexpr (sizeof(T) == 4) hipLaunchKernelGGL((one_kernel<T, 8>), grid, block, 0, stream, a);
+        static_assert((sizeof(T) == 4 ? 8 : 4) * round == kAcceptOne, "the largest takes every row");
         return hipGetLastError();
     }
     hipLaunchKernelGGL((sum_kernel<T>), dim3((unsigned)(a.num_seqs * (int64_t)a.pieces)), dim3(kThreads), 0,
                        stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((draw_kernel<T>), dim3((unsigned)a.num_seqs), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((draw_kernel<T>), dim3((unsigned)a.num_seqs), dim3(kOneThreads), 0, stream, a);
     return hipGetLastError();
 }
 
