@@ -402,6 +402,18 @@ typedef struct {
  * A zero-length sequence writes no output rows and copies its initial state (or zeros).
  * Nothing but out and final_state is written; neither may overlap an input (final_state may
  * be initial_state).
+ *
+ * fp32 inputs run token by token in fp32.  bf16 inputs run in chunks of 64 tokens; the state and
+ * every sum are fp32, and the products take fp16 operands: q and k, which bf16 holds exactly, and
+ * the fp32 side as a pair of 22 bits where it makes the state, as one of 11 bits in the readout
+ * (an eighth of the rounding of the output).  The rule is linear in (v, states), which are carried
+ * times eight: entries of v, of the states and of v - S^T k up to 8000 in size and of q and k up
+ * to 65504 stay finite (larger ones give non-finite results, not finite wrong ones); states keep
+ * 2^-22 of their size from 2e-3 up and 4e-9 below, outputs keep their rounding down to 1e-6.  q
+ * and k are meant to be of about unit norm.
+ * An input that is not finite reaches no other sequence and no other head, but within its chunk
+ * it may reach the outputs of earlier tokens: padding belongs behind the end of a sequence
+ * (cu_seqlens), where nothing is read.
  */
 kda_status kda_gdn_chunk_prefill(const kda_gdn_params* params, const void* q, const void* k,
                                  const void* v, const float* log_alpha, const float* beta,
@@ -428,6 +440,13 @@ kda_status kda_gdn_chunk_prefill(const kda_gdn_params* params, const void* q, co
  *                     entry do not matter.  Calls that share one must be ordered on one stream.
  * No output and not the workspace may overlap another argument.  Results do not depend on the
  * order in which the GPU runs the work: the same inputs give the same bits.
+ *
+ * Sums are fp32 (those over log-decays and of their gradients fp64).  fp32 inputs run token by
+ * token in fp32.  bf16 inputs run in chunks, with the forward's states as kda_gdn_chunk_prefill
+ * makes them (the same range of values) and with gradients at any scale: their side of a product
+ * is a pair of bf16 (16 bits), which measures below 1e-5 of a gradient's size in the fp32 outputs.
+ * The workspace takes 4 dk dv + 256 dv bytes per value head and 64 tokens, twice, and 8 dk bytes
+ * per value head and token where heads share a key head (bf16 inputs).
  */
 kda_status kda_gdn_prefill_backward(const kda_gdn_params* params, const void* q, const void* k,
                                     const void* v, const float* log_alpha, const float* beta,
@@ -457,6 +476,8 @@ int64_t kda_gdn_prefill_backward_workspace(const kda_gdn_params* params,
  *   state           : fp32 [num_slots, num_v_heads, dk, dv], read and written in place (only
  *                     read if update_state is 0)
  *   out             : may be NULL (no outputs); overlaps no other argument
+ * Everything is fp32 but the roundings of the inputs' and outputs' type.  The bits of a row depend
+ * on the batch's size (which fixes how a state is cut), not on the other rows' contents.
  */
 kda_status kda_gdn_recurrent(const kda_gdn_params* params, const void* q, const void* k,
                              const void* v, const float* log_alpha, const float* beta,
