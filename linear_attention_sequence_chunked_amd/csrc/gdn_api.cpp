@@ -289,7 +289,7 @@ kda_status kda_gdn_chunk_prefill(const kda_gdn_params* params, const void* q, co
         a.q = q; a.k = k; a.v = v; a.log_alpha = log_alpha; a.beta = beta;
         a.initial_state = initial_state; a.final_state = final_state; a.out = out;
         const bool chunked = d.dtype == KDA_DTYPE_BF16;
-        a.nv = chunked ? kda::gdn_prefill_nv(d.dv, pairs, cus) : 32;
+        a.nv = chunked ? kda::gdn_prefill_nv(d.dv, pairs, cus) : kda::gdn_sequential_nv(d.dv, pairs, cus);
         const std::vector<int32_t> order = longest_first(cu_seqlens_host, num_seqs);
         kda::GdnTable tab;
         for (int32_t from = 0; from < num_seqs; from += a.num_seqs) {

@@ -87,6 +87,8 @@ struct AcceptArgs {
 int gdn_recurrent_nv(int dv, int64_t pairs, int tokens, int cu_count);
 // value columns per workgroup of the chunked prefill (gdn_plan.cpp)
 int gdn_prefill_nv(int dv, int64_t pairs, int cu_count);
+// value columns per workgroup of the prefill of 32-bit inputs (gdn_plan.cpp)
+int gdn_sequential_nv(int dv, int64_t pairs, int cu_count);
 // sequences from place `from` of a table (longest first) on that share a launch of the chunks'
 // gradients; 0: none of them has a token (gdn_plan.cpp)
 int gdn_gradient_group(const GdnTable& t, int from, int n, int hv);

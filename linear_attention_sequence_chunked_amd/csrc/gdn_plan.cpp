@@ -28,6 +28,13 @@ int gdn_prefill_nv(int dv, int64_t pairs, int cu_count) {
     return nv;
 }
 
+int gdn_sequential_nv(int dv, int64_t pairs, int cu_count) {
+    // One column per lane while two workgroups per compute unit hold every state, else two, which
+    // share a token's operands.  1024 tokens, states of 128 x 128: 64 of them 226 us at one and 242
+    // at two, 128 of them 399 and 358, four 158 and 227.
+    return pairs * (dv / 16) <= 2 * cu_count ? 16 : 32;
+}
+
 int gdn_gradient_group(const GdnTable& t, int from, int n, int hv) {
     // A launch's grid is its longest sequence's chunks by its sequences, so shorter ones leave
     // workgroups without a chunk (0.34 ns each).  A group ends where those would cost as much as a

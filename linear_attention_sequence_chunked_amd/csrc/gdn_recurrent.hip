@@ -324,36 +324,39 @@ __global__ __launch_bounds__(kThreads, DK * NV == 128 * 128 ? 2 : 4) void decode
     if (out && rg == 0) store4(out + 4 * cg, Mma<T>::pack(fma4(kq, u, a * b)));  // (wave 0)
 }
 
-// The prefill of 32-bit inputs, token by token.  Each wave keeps eight columns of a state for the
-// whole sequence: lane (rg, cp) (rg = lane & 15) holds columns 2 cp, 2 cp + 1 of DK / 16
-// consecutive rows, so a column sum is four rotations within the 16 lanes of a DPP row and the
-// waves meet only once per 16 staged tokens (with a state's rows spread over four waves, as in
-// the step, the barrier and the shuffles through LDS take 0.73 us a token; this takes 0.22 at
-// dk = 64).  Narrow slices also spread few sequences over the card.  Bound by the dependent
-// chain of a token: two sums, the update, the next token's sums.
-template <int DK, int DV>
+// The prefill of 32-bit inputs, token by token.  Each wave keeps 4 CW columns of a state for the
+// whole sequence: lane (rg, cp) (rg = lane & 15) holds columns CW cp .. of DK / 16 consecutive
+// rows, so a column sum is four rotations within the 16 lanes of a DPP row and the waves meet
+// only once per 16 staged tokens (with a state's rows spread over four waves, as in the step, the
+// barrier and the shuffles through LDS take 0.73 us a token of 64 key channels; this takes 0.12,
+// 0.15 with 128).  Bound by the dependent chain of a token (sum, update, next token's sum) and
+// its issue: the readout's sum is taken behind the update, off that chain, the next token's
+// operands leave LDS a token ahead, and the tokens of a block are unrolled (0.19 in a loop).
+template <int DK, int DV, int CW>
 __global__ __launch_bounds__(kThreads) void seq_kernel(const RecArgs A, const GdnTable tab) {
-    constexpr int TB = 16, NV = 32, SL = DV / NV, R = DK / 16;
+    constexpr int TB = 16, NV = 16 * CW, SL = DV / NV, R = DK / 16;
     constexpr int QV = TB * DK / 4 / kThreads;
+    typedef float Cols __attribute__((ext_vector_type(CW)));
     __shared__ __attribute__((aligned(16))) float s_k[2][TB][DK], s_q[2][TB][DK], s_v[2][TB][NV], s_o[2][TB][NV];
     __shared__ float s_a[2][TB], s_b[2][TB];
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
     const int t = threadIdx.x, lane = t & 63, rg = lane & 15, cp = lane >> 4;
     const int64_t pair = blockIdx.x / SL;
     const int i = (int)(pair / A.hv), head = (int)(pair % A.hv), hk = head / (A.hv / A.hk), col0 = NV * (int)(blockIdx.x % SL);
-    const int col = 8 * (t / 64) + 2 * cp;  // of the slice
+    const int col = 4 * CW * (t / 64) + CW * cp;  // of the slice
     const int64_t start = tab.start[i], ss = ((int64_t)tab.id[i] * A.hv + head) * (int64_t)(DK * DV);
     const int len = tab.len[i];
     const int64_t at = ss + (int64_t)rg * R * DV + col0 + col;
-    f32x2 s[R];
+    Cols s[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        s[r] = A.S0 ? *reinterpret_cast<const f32x2*>(A.S0 + at + r * DV) : f32x2{0.f, 0.f};
-    // tokens on their way: rows of k and q, two entries of v, a gate
+    for (int r = 0; r < R; ++r) {
+        if (A.S0) s[r] = *reinterpret_cast<const Cols*>(A.S0 + at + r * DV);
+        else s[r] = Cols(0.f);
+    }
+    // tokens on their way: rows of k and q, CW entries of v, a gate
     f32x4 rk[QV], rq[QV];
-    f32x2 rv;
+    Cols rv;
     float rg_ = 0.f, rb = 0.f;
-    const int vr = t / 16, vc = 2 * (t % 16);
+    const int vr = t / 16, vc = CW * (t % 16);
     auto load = [&](int t0) {
 #pragma unroll
         for (int x = 0; x < QV; ++x) {
@@ -364,9 +367,9 @@ __global__ __launch_bounds__(kThreads) void seq_kernel(const RecArgs A, const Gd
                 rq[x] = load4f((const float*)A.q + (start + t0 + row) * A.qs + (int64_t)hk * DK + c);
             }
         }
-        rv = f32x2{0.f, 0.f};
+        rv = Cols(0.f);
         if (t0 + vr < len)
-            rv = *reinterpret_cast<const f32x2*>((const float*)A.v + (start + t0 + vr) * A.vs + (int64_t)head * DV + col0 + vc);
+            rv = *reinterpret_cast<const Cols*>((const float*)A.v + (start + t0 + vr) * A.vs + (int64_t)head * DV + col0 + vc);
         rg_ = rb = 0.f;
         if (t < TB && t0 + t < len) {
             rg_ = A.la[(start + t0 + t) * A.hv + head];
@@ -380,7 +383,7 @@ __global__ __launch_bounds__(kThreads) void seq_kernel(const RecArgs A, const Gd
             *reinterpret_cast<f32x4*>(&s_k[b][row][c]) = rk[x];
             *reinterpret_cast<f32x4*>(&s_q[b][row][c]) = rq[x] * A.scale;
         }
-        *reinterpret_cast<f32x2*>(&s_v[b][vr][vc]) = rv;
+        *reinterpret_cast<Cols*>(&s_v[b][vr][vc]) = rv;
         if (t < TB) {
             s_a[b][t] = expf(rg_);
             s_b[b][t] = rb;
@@ -393,59 +396,69 @@ __global__ __launch_bounds__(kThreads) void seq_kernel(const RecArgs A, const Gd
         x += dpp<0x121>(x);
         return x;
     };
+    auto store = [&](int t0) {  // a block's outputs: whole rows of the slice
+        if (t0 + vr < len)
+            *reinterpret_cast<Cols*>((float*)A.out + ((start + t0 + vr) * A.hv + head) * (int64_t)DV + col0 + vc) =
+                *reinterpret_cast<const Cols*>(&s_o[(t0 / TB) & 1][vr][vc]);
+    };
+    struct Token {
+        f32x4 k[R / 4], q[R / 4];
+        Cols v;
+        float a, b;
+    };
+    auto fetch = [&](int b, int j) {
+        Token x;
+#pragma unroll
+        for (int r = 0; r < R / 4; ++r) {
+            x.k[r] = *reinterpret_cast<const f32x4*>(&s_k[b][j][rg * R + 4 * r]);
+            x.q[r] = *reinterpret_cast<const f32x4*>(&s_q[b][j][rg * R + 4 * r]);
+        }
+        x.v = *reinterpret_cast<const Cols*>(&s_v[b][j][col]);
+        x.a = s_a[b][j];
+        x.b = s_b[b][j];
+        return x;
+    };
     load(0);
     for (int t0 = 0; t0 < len; t0 += TB) {
-        const int b = (t0 / TB) & 1, m = min(len - t0, TB);
+        const int b = (t0 / TB) & 1;
         put(b);
         lds_barrier();
-        if (t0 > 0) {  // the block before: whole rows of the slice
-            *reinterpret_cast<f32x2*>((float*)A.out + ((start + t0 - TB + vr) * A.hv + head) * (int64_t)DV + col0 + vc) =
-                *reinterpret_cast<const f32x2*>(&s_o[1 - b][vr][vc]);
-        }
+        if (t0 > 0) store(t0 - TB);
         load(t0 + TB);
-        for (int j = 0; j < m; ++j) {
-            float k[R], q[R];
+        // Rows behind the last token are zeros with a = 1 and b = 0 and leave the state as it is,
+        // so a block is always whole and its loop unrolled.  Lane rg keeps token rg's outputs.
+        Token x = fetch(b, 0);
+        Cols mine = Cols(0.f);
+        unroll<0, TB>([&](auto J) {
+            constexpr int j = decltype(J)::value;
+            Token y = x;
+            if constexpr (j + 1 < TB) y = fetch(b, j + 1);
+            Cols w = Cols(0.f), o = Cols(0.f);
 #pragma unroll
-            for (int r = 0; r < R; r += 4) {
-                const f32x4 kk = *reinterpret_cast<const f32x4*>(&s_k[b][j][rg * R + r]);
-                const f32x4 qq = *reinterpret_cast<const f32x4*>(&s_q[b][j][rg * R + r]);
+            for (int r = 0; r < R; ++r) w += s[r] * x.k[r / 4][r % 4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    k[r + x] = kk[x];
-                    q[r + x] = qq[x];
-                }
-            }
-            f32x2 w = {0.f, 0.f}, o = {0.f, 0.f};
-            float kq = 0.f;
+            for (int c = 0; c < CW; ++c) w[c] = sum16(w[c]);
+            const Cols u = x.b * (x.v - x.a * w);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                w += s[r] * k[r];
-                o += s[r] * q[r];
-                kq = fmaf(k[r], q[r], kq);
+                s[r] = x.a * s[r] + x.k[r / 4][r % 4] * u;
+                o += s[r] * x.q[r / 4][r % 4];
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                w[c] = sum16(w[c]);
-                o[c] = sum16(o[c]);
+            for (int c = 0; c < CW; ++c) {
+                const float sum = sum16(o[c]);
+                mine[c] = rg == j ? sum : mine[c];
             }
-            kq = sum16(kq);
-            const float a = s_a[b][j];
-            const f32x2 u = s_b[b][j] * (*reinterpret_cast<const f32x2*>(&s_v[b][j][col]) - a * w);
-#pragma unroll
-            for (int r = 0; r < R; ++r) s[r] = a * s[r] + k[r] * u;
-            if (rg == 0) *reinterpret_cast<f32x2*>(&s_o[b][j][col]) = a * o + kq * u;
-        }
+            x = y;
+            __builtin_amdgcn_sched_barrier(0);  // (operands one token ahead, not more: registers)
+        });
+        *reinterpret_cast<Cols*>(&s_o[b][rg][col]) = mine;
     }
     lds_barrier();
-    if (len > 0) {  // the last block's outputs
-        const int t0 = (len - 1) / TB * TB;
-        if (t0 + vr < len)
-            *reinterpret_cast<f32x2*>((float*)A.out + ((start + t0 + vr) * A.hv + head) * (int64_t)DV + col0 + vc) =
-                *reinterpret_cast<const f32x2*>(&s_o[(t0 / TB) & 1][vr][vc]);
-    }
+    if (len > 0) store((len - 1) / TB * TB);
     if (A.Sf) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) *reinterpret_cast<f32x2*>(A.Sf + at + r * DV) = s[r];
+        for (int r = 0; r < R; ++r) *reinterpret_cast<Cols*>(A.Sf + at + r * DV) = s[r];
     }
 }
 
@@ -501,15 +514,21 @@ hipError_t launch_gdn_sequential(const GdnPrefillArgs& a, const GdnTable& tab, h
     RecArgs r = common(a.d);
     r.q = a.q; r.k = a.k; r.v = a.v; r.la = a.log_alpha; r.be = a.beta; r.out = a.out;
     r.S0 = a.initial_state; r.Sf = a.final_state;
-    const int64_t blocks = (int64_t)a.num_seqs * a.d.hv * (a.d.dv / 32);
+    const int64_t blocks = (int64_t)a.num_seqs * a.d.hv * (a.d.dv / a.nv);
     if (a.d.dtype != DTYPE_F32) return hipErrorInvalidValue;
     if (blocks == 0) return hipSuccess;
-    const dim3 grid((unsigned)blocks), block(kThreads);
-    if (a.d.dk == 128 && a.d.dv == 128) hipLaunchKernelGGL((seq_kernel<128, 128>), grid, block, 0, stream, r, tab);
-    else if (a.d.dk == 128) hipLaunchKernelGGL((seq_kernel<128, 64>), grid, block, 0, stream, r, tab);
-    else if (a.d.dv == 128) hipLaunchKernelGGL((seq_kernel<64, 128>), grid, block, 0, stream, r, tab);
-    else hipLaunchKernelGGL((seq_kernel<64, 64>), grid, block, 0, stream, r, tab);
-    return hipGetLastError();
+    auto go = [&](auto dk, auto dv, auto cw) {
+        hipLaunchKernelGGL((seq_kernel<decltype(dk)::value, decltype(dv)::value, decltype(cw)::value>), dim3((unsigned)blocks),
+                           dim3(kThreads), 0, stream, r, tab);
+        return hipGetLastError();
+    };
+    auto widths = [&](auto dk, auto dv) {
+        return a.nv == 16 ? go(dk, dv, std::integral_constant<int, 1>{}) : go(dk, dv, std::integral_constant<int, 2>{});
+    };
+    auto values = [&](auto dk) {
+        return a.d.dv == 128 ? widths(dk, std::integral_constant<int, 128>{}) : widths(dk, std::integral_constant<int, 64>{});
+    };
+    return a.d.dk == 128 ? values(std::integral_constant<int, 128>{}) : values(std::integral_constant<int, 64>{});
 }
 
 }  // namespace kda
