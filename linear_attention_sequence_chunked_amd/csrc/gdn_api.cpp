@@ -134,21 +134,26 @@ int32_t fill_table(kda::GdnTable& t, const int32_t* cu, const std::vector<int32_
 
 uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
-// Workspace of the backward: parts of dq and dk (shared key heads only), then what the form
-// needs.  In chunks (bf16): per chunk and value head the state before it, the gradient of the
+// Workspace of the backward: parts of dq and dk (shared key heads, or states cut in slices; those
+// have parts of the gates' gradients too), then what the form needs.  In chunks (bf16): per chunk and value head the state before it, the gradient of the
 // state behind it, U and dX, four bytes an element; at most T/64 + num_seqs chunks per head.
-// Token by token: at most T/16 + num_seqs states per value head, and 16 states for each
-// workgroup that runs at once.
+// Token by token: at most T/16 + num_seqs states per value head, and 16 slices of a state for
+// each workgroup that runs at once.
 struct BwdPlan {
-    uint64_t parts = 0, off_k = 0, off_a = 0, off_b = 0, off_c = 0, off_d = 0, total = 0;
-    int slots = 0;
+    uint64_t parts = 0, off_k = 0, off_g = 0, off_e = 0, off_a = 0, off_b = 0, off_c = 0, off_d = 0, total = 0;
+    int slots = 0, slices = 1;
 };
 BwdPlan plan_backward(const kda::GdnDims& d, const int32_t* cu, int32_t n) {
     BwdPlan p;
     const uint64_t T = (uint64_t)cu[n], hv = (uint64_t)d.hv, state = 4ull * d.dk * d.dv;
-    if (d.hv != d.hk) p.parts = align256(T * hv * d.dk * 4);
+    const int cus = kda::device_cu_count();
+    if (d.dtype == KDA_DTYPE_F32) p.slices = kda::gdn_backward_seq_slices(d.dv, (int64_t)n * d.hv, cus);
+    if (d.hv != d.hk || p.slices > 1) p.parts = align256(T * hv * p.slices * d.dk * 4);
+    const uint64_t gates = p.slices > 1 ? align256(T * hv * p.slices * 4) : 0;
     p.off_k = p.parts;
-    p.off_a = 2 * p.parts;
+    p.off_g = 2 * p.parts;
+    p.off_e = p.off_g + gates;
+    p.off_a = p.off_e + gates;
     if (d.dtype == KDA_DTYPE_BF16) {
         const uint64_t chunks = (T / 64 + n) * hv, rows = 4ull * 64 * d.dv;
         p.off_b = p.off_a + align256(chunks * state);
@@ -157,9 +162,9 @@ BwdPlan plan_backward(const kda::GdnDims& d, const int32_t* cu, int32_t n) {
         p.total = p.off_d + align256(chunks * rows);
         return p;
     }
-    p.slots = (int)std::min<int64_t>((int64_t)std::min(n, kda::kGdnSeqs) * d.hv, 2 * kda::device_cu_count());
+    p.slots = (int)std::min<int64_t>((int64_t)std::min(n, kda::kGdnSeqs) * d.hv * p.slices, 2 * cus);
     p.off_b = p.off_a + align256((T / 16 + n) * hv * state);
-    p.total = p.off_b + (uint64_t)p.slots * 16 * state;
+    p.total = p.off_b + (uint64_t)p.slots * 16 * (state / p.slices);
     return p;
 }
 
@@ -232,6 +237,9 @@ kda_status kda_gdn_prefill_backward(const kda_gdn_params* params, const void* q,
         a.parts = plan.parts > 0;
         a.dq_parts = reinterpret_cast<float*>(ws);
         a.dk_parts = reinterpret_cast<float*>(ws + plan.off_k);
+        a.dg_parts = reinterpret_cast<float*>(ws + plan.off_g);
+        a.db_parts = reinterpret_cast<float*>(ws + plan.off_e);
+        a.slices = plan.slices;
         const bool chunked = d.dtype == KDA_DTYPE_BF16;
         if (chunked) {
             a.states = ws + plan.off_a; a.sgrads = ws + plan.off_b; a.u = ws + plan.off_c; a.dx = ws + plan.off_d;

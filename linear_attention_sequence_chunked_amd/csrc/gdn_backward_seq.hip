@@ -11,17 +11,17 @@
 // token's read during this one's sums), so no state is ever divided by its decay.  Everything is
 // fp32.
 //
-// One workgroup of four waves holds a whole state: thread t has columns 4 (t % COLG) .. +3 of
+// One workgroup of four waves holds a state, or 32 of its columns: thread t has columns 4 (t % COLG) .. +3 of
 // RPT consecutive rows.  Column sums (du) go through LDS, one barrier per token; row sums
 // (dq, dk) are reduced among the COLG threads of a row group, halving the rows at each step; the
 // gates' sums over the state (dg, dbeta) are kept per thread and added once per block.
-// States of 128 x 128: 4.3 us a token, of which about 2.5 are the issue of some 1500 vector
-// instructions by each of the four SIMDs (two walks forwards, one backwards), the rest LDS and
-// barriers; 6.6 with a state on each of 256 compute units, where the scratch's 128 KiB a token
-// come from beyond L2 at 5 TB/s.
+// States of 128 x 128: up to 64 of them, in slices, 2.2 to 2.6 us a token, latency of the three
+// walks' sums and barriers; whole ones 4.3, of which about 2.5 are the issue of some 1500 vector
+// instructions by each of the four SIMDs; 6.6 with a state on each of 256 compute units, where
+// the scratch's 128 KiB a token come from beyond L2 at 5 TB/s.
 //
-// Heads that share a key head write their parts of dq and dk apart; a second launch adds them
-// in head order.
+// Heads that share a key head, and slices, write their parts of dq and dk apart; a second launch
+// adds them in order (and a third the gates' of the slices).
 #include <algorithm>
 
 #include "gdn_launch.h"
@@ -37,10 +37,11 @@ constexpr int TB = 16;
 
 __device__ inline f32x4 load4f(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 
-template <int DK, int DV>
+// NV columns of a state in one workgroup
+template <int DK, int DV, int NV>
 struct Shape {
-    static constexpr int COLG = DV / 4, ROWG = kThreads / COLG, RPT = DK / ROWG;
-    static constexpr int64_t STATE = (int64_t)DK * DV;
+    static constexpr int COLG = NV / 4, ROWG = kThreads / COLG, RPT = DK / ROWG, SL = DV / NV;
+    static constexpr int64_t STATE = (int64_t)DK * DV, OWN = (int64_t)DK * NV;
 };
 
 // x of the lane whose number differs in bit OFF: one DPP move, or a trip through LDS for 4 and 16
@@ -56,19 +57,23 @@ __device__ inline float partner(float x) {
 // thread returns the sum of value `row`, chosen by the lane bits that the halvings took
 // (kTaken<N>).  (A recursion: in a loop whose bound halves the compiler keeps the array's indexes
 // dynamic, a select per element and access, which took 8.7 of 13.5 us a token.)
-constexpr int kOff[5] = {1, 2, 8, 4, 16};  // the moves first
+template <int LANES>
+constexpr int offset(int step) {  // the moves first
+    constexpr int few[3] = {1, 2, 4}, many[5] = {1, 2, 8, 4, 16};
+    return LANES == 8 ? few[step] : many[step];
+}
 template <int N>
-constexpr int kTaken = N == 16 ? 15 : N == 8 ? 11 : 3;
+constexpr int kTaken = N == 16 ? 15 : N == 8 ? 11 : N - 1;
 template <int N, int LANES, int STEP = 0>
 __device__ inline float reduce_rows(const float (&v)[N], int c, int& row) {
-    constexpr int OFF = kOff[STEP < 5 ? STEP : 0];
-    if constexpr (N == 1) {
-        if constexpr (STEP == 5 || (1 << STEP) == LANES) return v[0];
-        else {
-            const float x[1] = {v[0] + partner<OFF>(v[0])};
-            return reduce_rows<1, LANES, STEP + 1>(x, c, row);
-        }
+    if constexpr ((1 << STEP) == LANES) {
+        static_assert(N == 1, "no more values than lanes");
+        return v[0];
+    } else if constexpr (N == 1) {
+        const float x[1] = {v[0] + partner<offset<LANES>(STEP)>(v[0])};
+        return reduce_rows<1, LANES, STEP + 1>(x, c, row);
     } else {
+        constexpr int OFF = offset<LANES>(STEP);
         const bool up = c & OFF;
         float h[N / 2];
 #pragma unroll
@@ -89,19 +94,20 @@ __device__ inline float sum16(float x) {  // over the row of 16 lanes
     return x;
 }
 
-template <int DK, int DV>
-__global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArgs A, const GdnTable tab, int pairs) {
-    using L = Shape<DK, DV>;
-    constexpr int COLG = L::COLG, RPT = L::RPT;
-    __shared__ __attribute__((aligned(16))) float s_k[TB][DK], s_q[TB][DK], s_v[TB][DV], s_do[TB][DV], s_err[TB][DV];
+template <int DK, int DV, int NV>
+__global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArgs A, const GdnTable tab, int units) {
+    using L = Shape<DK, DV, NV>;
+    constexpr int COLG = L::COLG, RPT = L::RPT, SL = L::SL;
+    __shared__ __attribute__((aligned(16))) float s_k[TB][DK], s_q[TB][DK], s_v[TB][NV], s_do[TB][NV], s_err[TB][NV];
     __shared__ float s_a[TB], s_b[TB], s_g[TB][kThreads], s_db[TB][COLG];
     __shared__ f32x4 s_red[2][4][COLG];
     const int t = threadIdx.x, cg = t % COLG, rg = t / COLG, wave = t / 64, lane = t % 64;
-    float* scratch = A.scratch + (int64_t)blockIdx.x * TB * L::STATE;
-    const int64_t at = (int64_t)(rg * RPT) * DV + 4 * cg;
+    float* scratch = A.scratch + (int64_t)blockIdx.x * TB * L::OWN + (rg * RPT) * NV + 4 * cg;
     const GdnDims& d = A.d;
 
-    for (int pair = blockIdx.x; pair < pairs; pair += gridDim.x) {
+    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int pair = unit / SL, slice = unit % SL, col0 = NV * slice;
+        const int64_t at = (int64_t)(rg * RPT) * DV + col0 + 4 * cg;
         const int si = pair / d.hv, h = pair % d.hv, hk = h / (d.hv / d.hk), len = tab.len[si], id = tab.id[si];
         const int64_t start = tab.start[si], ss = ((int64_t)id * d.hv + h) * L::STATE;
         // the state before block b of this sequence and head
@@ -122,12 +128,12 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
                 *reinterpret_cast<f32x4*>(&s_k[r][c]) = kv;
                 *reinterpret_cast<f32x4*>(&s_q[r][c]) = qv * d.scale;
             }
-            for (int e = t; e < TB * DV / 4; e += kThreads) {
-                const int r = e / (DV / 4), c = 4 * (e % (DV / 4));
+            for (int e = t; e < TB * NV / 4; e += kThreads) {
+                const int r = e / (NV / 4), c = 4 * (e % (NV / 4));
                 f32x4 vv = zero4(), ov = zero4();
                 if (r < m) {
-                    vv = load4f((const float*)A.v + (row0 + r) * d.vs + (int64_t)h * DV + c);
-                    ov = load4f((const float*)A.d_out + ((row0 + r) * d.hv + h) * (int64_t)DV + c);
+                    vv = load4f((const float*)A.v + (row0 + r) * d.vs + (int64_t)h * DV + col0 + c);
+                    ov = load4f((const float*)A.d_out + ((row0 + r) * d.hv + h) * (int64_t)DV + col0 + c);
                 }
                 *reinterpret_cast<f32x4*>(&s_v[r][c]) = vv;
                 *reinterpret_cast<f32x4*>(&s_do[r][c]) = ov;
@@ -162,7 +168,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
                 for (int i = 0; i < RPT; ++i) {
                     S[i] *= s_a[j];
                     w += S[i] * s_k[j][rg * RPT + i];
-                    if (save) *reinterpret_cast<f32x4*>(scratch + j * L::STATE + at + i * DV) = S[i];
+                    if (save) *reinterpret_cast<f32x4*>(scratch + j * L::OWN + i * NV) = S[i];
                 }
                 w = column_sum(w);
                 const f32x4 err = *reinterpret_cast<const f32x4*>(&s_v[j][4 * cg]) - w;
@@ -191,7 +197,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
             lds_barrier();
             auto decayed = [&](int j) {
 #pragma unroll
-                for (int i = 0; i < RPT; ++i) S[i] = *reinterpret_cast<const f32x4*>(scratch + j * L::STATE + at + i * DV);
+                for (int i = 0; i < RPT; ++i) S[i] = *reinterpret_cast<const f32x4*>(scratch + j * L::OWN + i * NV);
             };
             decayed(m - 1);
             for (int j = m - 1; j >= 0; --j) {
@@ -222,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
                 int row = 0, same = 0;
                 const float rq = reduce_rows<RPT, COLG>(pq, cg, row), rk = reduce_rows<RPT, COLG>(pk, cg, same);
                 if ((cg & ~kTaken<RPT>) == 0) {
-                    const int64_t o = (A.parts ? ((row0 + j) * d.hv + h) : ((row0 + j) * d.hk + hk)) * (int64_t)DK + rg * RPT + row;
+                    const int64_t o = (A.parts ? ((row0 + j) * d.hv + h) * SL + slice : (row0 + j) * d.hk + hk) * (int64_t)DK + rg * RPT + row;
                     if (A.parts) {
                         A.dq_parts[o] = d.scale * rq;
                         A.dk_parts[o] = rk;
@@ -233,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
                 }
                 s_g[j][t] = dg;  // summed over the threads behind the block
                 if (rg == 0) {
-                    *reinterpret_cast<f32x4*>((float*)A.dv + ((row0 + j) * d.hv + h) * (int64_t)DV + 4 * cg) = bdu;
+                    *reinterpret_cast<f32x4*>((float*)A.dv + ((row0 + j) * d.hv + h) * (int64_t)DV + col0 + 4 * cg) = bdu;
                     s_db[j][cg] = dot(du, err);
                 }
             }
@@ -244,12 +250,13 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
 #pragma unroll
                 for (int i = 0; i < kThreads / 16; ++i) x += s_g[j][l + 16 * i];
 #pragma unroll
-                for (int i = 0; i < COLG / 16; ++i) y += s_db[j][l + 16 * i];
+                for (int i = 0; i < COLG; i += 16) y += i + l < COLG ? s_db[j][i + l] : 0.f;
                 x = sum16(x);
                 y = sum16(y);
                 if (l == 0 && j < m) {
-                    A.dlog_alpha[(row0 + j) * d.hv + h] = x;
-                    A.dbeta[(row0 + j) * d.hv + h] = y;
+                    const int64_t o = ((row0 + j) * d.hv + h) * SL + slice;
+                    (SL > 1 ? A.dg_parts : A.dlog_alpha)[o] = x;
+                    (SL > 1 ? A.db_parts : A.dbeta)[o] = y;
                 }
             }
         }
@@ -261,45 +268,65 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(const GdnBackwardArg
     }
 }
 
-// dq and dk of a key head: the sums over the value heads that share it, in head order
+// dq and dk of a key head: the sums over the parts of it (the value heads that share it, and the
+// slices of their columns), in order
 template <typename T>
-__global__ __launch_bounds__(256) void sum_parts_kernel(const GdnBackwardArgs A, int64_t total4, int dk4) {
+__global__ __launch_bounds__(256) void sum_parts_kernel(const GdnBackwardArgs A, int64_t total4, int dk4, int parts) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= total4) return;
-    const int group = A.d.hv / A.d.hk;
     const int64_t c = i % dk4, th = i / dk4;  // th: token and key head
-    const int64_t src = th * group * dk4 + c;
+    const int64_t src = th * parts * dk4 + c;
     f32x4 q = zero4(), k = zero4();
-    for (int n = 0; n < group; ++n) {
+    for (int n = 0; n < parts; ++n) {
         q += reinterpret_cast<const f32x4*>(A.dq_parts)[src + (int64_t)n * dk4];
         k += reinterpret_cast<const f32x4*>(A.dk_parts)[src + (int64_t)n * dk4];
     }
     store4((T*)A.dq + 4 * i, Mma<T>::pack(q));
     store4((T*)A.dk + 4 * i, Mma<T>::pack(k));
 }
+// the gates' gradients: sums over the slices
+__global__ __launch_bounds__(256) void sum_gates_kernel(const GdnBackwardArgs A, int64_t total, int slices) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total) return;
+    float g = 0.f, b = 0.f;
+    for (int n = 0; n < slices; ++n) {
+        g += A.dg_parts[i * slices + n];
+        b += A.db_parts[i * slices + n];
+    }
+    A.dlog_alpha[i] = g;
+    A.dbeta[i] = b;
+}
 
 template <typename T>
 hipError_t sum_parts(const GdnBackwardArgs& a, hipStream_t st) {
-    const int64_t total4 = a.T * a.d.hk * (a.d.dk / 4);
+    const int64_t total4 = a.T * a.d.hk * (a.d.dk / 4), gates = a.T * a.d.hv;
     if (total4 == 0) return hipSuccess;
-    hipLaunchKernelGGL((sum_parts_kernel<T>), dim3((unsigned)((total4 + 255) / 256)), dim3(256), 0, st, a, total4, a.d.dk / 4);
+    hipLaunchKernelGGL((sum_parts_kernel<T>), dim3((unsigned)((total4 + 255) / 256)), dim3(256), 0, st, a, total4, a.d.dk / 4,
+                       a.d.hv / a.d.hk * a.slices);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.slices == 1) return e;
+    hipLaunchKernelGGL(sum_gates_kernel, dim3((unsigned)((gates + 255) / 256)), dim3(256), 0, st, a, gates, a.slices);
     return hipGetLastError();
 }
 
-template <int DK, int DV>
+template <int DK, int DV, int NV>
 hipError_t launch(const GdnBackwardArgs& a, const GdnTable& tab, hipStream_t st) {
-    const int pairs = a.num_seqs * a.d.hv;
-    if (pairs == 0) return hipSuccess;
-    hipLaunchKernelGGL((backward_kernel<DK, DV>), dim3((unsigned)std::min(pairs, a.slots)), dim3(kThreads), 0, st, a, tab, pairs);
+    const int units = a.num_seqs * a.d.hv * (DV / NV);
+    if (units == 0) return hipSuccess;
+    hipLaunchKernelGGL((backward_kernel<DK, DV, NV>), dim3((unsigned)std::min(units, a.slots)), dim3(kThreads), 0, st, a, tab, units);
     return hipGetLastError();
+}
+template <int DK, int DV>
+hipError_t launch_nv(const GdnBackwardArgs& a, const GdnTable& tab, hipStream_t st) {
+    return a.slices > 1 ? launch<DK, DV, 32>(a, tab, st) : launch<DK, DV, DV>(a, tab, st);
 }
 
 }  // namespace
 
 hipError_t launch_gdn_backward_seq(const GdnBackwardArgs& a, const GdnTable& tab, hipStream_t st) {
     if (a.d.dtype != DTYPE_F32) return hipErrorInvalidValue;
-    if (a.d.dk == 128) return a.d.dv == 128 ? launch<128, 128>(a, tab, st) : launch<128, 64>(a, tab, st);
-    return a.d.dv == 128 ? launch<64, 128>(a, tab, st) : launch<64, 64>(a, tab, st);
+    if (a.d.dk == 128) return a.d.dv == 128 ? launch_nv<128, 128>(a, tab, st) : launch_nv<128, 64>(a, tab, st);
+    return a.d.dv == 128 ? launch_nv<64, 128>(a, tab, st) : launch_nv<64, 64>(a, tab, st);
 }
 
 hipError_t launch_gdn_sum_parts(const GdnBackwardArgs& a, hipStream_t st) {

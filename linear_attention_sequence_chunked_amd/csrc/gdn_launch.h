@@ -60,9 +60,11 @@ struct GdnBackwardArgs {
     void *dq, *dk, *dv;
     float *dlog_alpha, *dbeta;
     float* d_initial_state;       // may be null
-    bool parts;                   // shared key heads: dq and dk of each value head apart first
-    float *dq_parts, *dk_parts;   // [T, hv, dk]
-    // token by token: states before every 16th token, and a scratch of 16 states per workgroup
+    bool parts;                   // dq and dk of each value head (and slice) apart first
+    int slices;                   // of a state's columns, over workgroups (token by token; else 1)
+    float *dq_parts, *dk_parts;   // [T, hv, slices, dk]
+    float *dg_parts, *db_parts;   // [T, hv, slices], several slices alone
+    // token by token: states before every 16th token, and a scratch of 16 slices per workgroup
     float *checkpoints, *scratch;
     int slots;                    // workgroups the scratch serves
     // in chunks: per (chunk, value head) the states, their gradients, U and dX (gdn_chunk.h)
@@ -89,6 +91,8 @@ int gdn_recurrent_nv(int dv, int64_t pairs, int tokens, int cu_count);
 int gdn_prefill_nv(int dv, int64_t pairs, int cu_count);
 // value columns per workgroup of the prefill of 32-bit inputs (gdn_plan.cpp)
 int gdn_sequential_nv(int dv, int64_t pairs, int cu_count);
+// slices of a state's columns in the token-by-token gradients (gdn_plan.cpp)
+int gdn_backward_seq_slices(int dv, int64_t pairs, int cu_count);
 // sequences from place `from` of a table (longest first) on that share a launch of the chunks'
 // gradients; 0: none of them has a token (gdn_plan.cpp)
 int gdn_gradient_group(const GdnTable& t, int from, int n, int hv);

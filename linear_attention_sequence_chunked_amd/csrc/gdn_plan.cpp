@@ -35,6 +35,13 @@ int gdn_sequential_nv(int dv, int64_t pairs, int cu_count) {
     return pairs * (dv / 16) <= 2 * cu_count ? 16 : 32;
 }
 
+int gdn_backward_seq_slices(int dv, int64_t pairs, int cu_count) {
+    // Slices of 32 columns while two workgroups per compute unit hold every state; whole states
+    // else, whose sums over rows need no second launch.  512 tokens, states of 128 x 128: 16 of
+    // them 1.18 ms in slices and 2.26 whole, 128 of them 1.94 and 2.56, 256 3.73 and 3.39.
+    return pairs * (dv / 32) <= 2 * cu_count ? dv / 32 : 1;
+}
+
 int gdn_gradient_group(const GdnTable& t, int from, int n, int hv) {
     // A launch's grid is its longest sequence's chunks by its sequences, so shorter ones leave
     // workgroups without a chunk (0.34 ns each).  A group ends where those would cost as much as a

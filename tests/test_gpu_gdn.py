@@ -57,6 +57,13 @@ def test_prefill_more_sequences_than_one_launch(dtype):
     check_prefill(x, cu, DT[dtype])
 
 
+@pytest.mark.parametrize("dk,dv,n", [(64, 128, 70), (128, 64, 130), (128, 128, 70)])
+def test_prefill_f32_of_many_states(dk, dv, n):
+    """More states than one column per lane would fill the card with."""
+    x, cu = ref.inputs([(11 * i) % 37 for i in range(n)], 1, 1, dk, dv, torch.float32, seed=n)
+    check_prefill(x, cu, torch.float32)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prefill_all_empty(dtype):
     x, cu = ref.inputs([0, 0], 1, 2, 64, 64, DT[dtype], seed=3)

@@ -74,6 +74,13 @@ def test_backward_many_sequences(dtype):
     check(x, cu, DT[dtype])
 
 
+@pytest.mark.parametrize("dk,dv,n", [(64, 128, 132), (128, 64, 260), (128, 128, 132)])
+def test_backward_f32_of_many_states(dk, dv, n):
+    """More states than slices of them would fill the card with."""
+    x, cu = ref.inputs([(7 * i) % 19 for i in range(n)], 1, 1, dk, dv, F32, seed=n)
+    check(x, cu, F32)
+
+
 def test_backward_one_long_sequence_among_short_ones():
     """Lengths so far apart that the chunks' gradients take several launches."""
     x, cu = ref.inputs([3] * 150 + [700, 0] + [2] * 100 + [65], 1, 16, 64, 64, torch.bfloat16, seed=10)
