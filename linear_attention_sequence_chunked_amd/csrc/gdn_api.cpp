@@ -417,6 +417,7 @@ kda_status kda_spec_accept(int32_t dtype, int32_t num_seqs, int32_t num_draft, i
     a.pieces = kda::accept_pieces(num_seqs, vocab, kda::device_cu_count());
     a.piece = (vocab + a.pieces - 1) / a.pieces;
     if ((st = check_grid((int64_t)num_seqs * a.pieces, 256)) != KDA_OK) return st;
+    if ((st = check_grid(num_seqs, 1024)) != KDA_OK) return st;
     const hipError_t e = kda::launch_accept(a, reinterpret_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(KDA_ERR_HIP, "kda_spec_accept launch: %s", hipGetErrorString(e));
     return kda::ok();

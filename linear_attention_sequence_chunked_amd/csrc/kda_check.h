@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <string>
@@ -55,16 +56,16 @@ inline kda_status check_ptr(const char* name, const void* ptr, size_t align) {
 }
 
 inline int device_cu_count() {
-    static int cached = 0;
-    if (cached) return cached;
+    static std::atomic<int> cached{0};  // calls may come from several threads
+    if (const int known = cached.load(std::memory_order_relaxed)) return known;
     int dev = 0, cus = 0;
     if (hipGetDevice(&dev) == hipSuccess &&
         hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess &&
         cus > 0)
-        cached = cus;
+        cached.store(cus, std::memory_order_relaxed);
     else
-        cached = 256;
-    return cached;
+        cached.store(cus = 256, std::memory_order_relaxed);
+    return cus;
 }
 
 }  // namespace kda

@@ -115,6 +115,8 @@ def test_launches_beyond_the_grid_are_refused():
     far = dict(q=1 << 54, k=1 << 55, v=1 << 56, la=1 << 57, be=1 << 58, out=1 << 59)
     st, msg = recurrent(p, n=1 << 12, slots=0, idx=1 << 53, state=None, upd=0, **far)
     assert st == UNS and "workgroups exceed one launch" in msg
+    st, msg = accept(n=1 << 23, k=0, vocab=8, p=1 << 54, q=None, x=None, u=1 << 55, acc=1 << 56, tok=1 << 57, ws=1 << 58, nb=1 << 40)
+    assert st == UNS and "workgroups exceed one launch" in msg
 
 
 # ------------------------------------------------------------------------------ the binding
