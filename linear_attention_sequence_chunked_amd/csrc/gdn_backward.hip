@@ -574,13 +574,14 @@ __global__ __launch_bounds__(256, 2) void gdn_gradients_kernel(const GdnBackward
     for (int b = 0; b < C::KW / 2; ++b) tr[b] = zero4();
     float xv = 0.f;
     load(0);
+    const int slices = d.dv / 32;  // (as a constant, two of them are unrolled into spilled registers)
 #pragma unroll 1
-    for (int n = 0; n < DV / 32; ++n) {
+    for (int n = 0; n < slices; ++n) {
         lds_barrier();
         put();
         const u32x2 vcur[2] = {y.v[0], y.v[1]};
         lds_barrier();
-        if (n + 1 < DV / 32) load(n + 1);
+        if (n + 1 < slices) load(n + 1);
         // (the scheduling barriers keep operands from being read further ahead than fits the
         // registers)
         bf16x8 xh[2], xl[2];
