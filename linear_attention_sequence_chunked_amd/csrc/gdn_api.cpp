@@ -74,7 +74,7 @@ kda_status check_grid(int64_t blocks, int64_t threads) {
 }
 
 // the (sequence, head) pairs of one launch, their columns cut finest, at most 1024 threads each
-// (704 and two walks in the gradients' first)
+// (768 and two walks in the gradients' first)
 kda_status check_pairs(const kda::GdnDims& d, int32_t num_seqs) {
     return check_grid(2 * ((int64_t)std::min(num_seqs, kda::kGdnSeqs) * d.hv * (d.dv / 16) + 64), 1024);
 }

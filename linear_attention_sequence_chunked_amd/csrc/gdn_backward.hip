@@ -48,8 +48,8 @@ constexpr int NCB = 2;
 template <int DK>
 struct WCfg {
     static constexpr int KB = DK / 16, KP = DK / 32, NV = 16 * NCB;
-    // wave numbers: chain (one per 16 columns), stage (4), inverse (2), gram (2)
-    static constexpr int W_STAGE = NCB, W_INV = W_STAGE + 4, W_GRAM = W_INV + 2, THREADS = 64 * (W_GRAM + 2);
+    // wave numbers: chain (one per 16 columns), stage (4), inverse (2), gram (2), gates
+    static constexpr int W_STAGE = NCB, W_INV = W_STAGE + 4, W_GRAM = W_INV + 2, W_GATE = W_GRAM + 2, THREADS = 64 * (W_GATE + 1);
     typedef KeyTile<DK> K;
     typedef ValueTile<NV> V;
     // fragments (a pair: hi, lo): T^T's halves, -A^T's block, P^T's three blocks, two row tiles each
@@ -109,7 +109,7 @@ __device__ __forceinline__ void gdn_walk_back(const WArgs& a, const GdnTable& ta
             lds_barrier();
         }
     };
-    if (wave >= C::W_GRAM + 2) {  // the forward walk has a wave more: this one keeps the barriers
+    if (wave > C::W_GATE) {  // the forward walk has a wave more: this one keeps the barriers
         for (int c = 0; c < passes; ++c) {
             lds_barrier();
             lds_barrier();
@@ -119,7 +119,6 @@ __device__ __forceinline__ void gdn_walk_back(const WArgs& a, const GdnTable& ta
     if (wave >= C::W_STAGE && wave < C::W_INV) {
         struct Staged {
             u32x4 k[C::K::PPT], q[C::K::PPT], o[C::V::PPT];
-            float la, be;
         };
         Staged x[R];
         const int st = tid - 64 * C::W_STAGE;
@@ -128,12 +127,9 @@ __device__ __forceinline__ void gdn_walk_back(const WArgs& a, const GdnTable& ta
             // its use)
             const int rows = c < nch ? min(kGC, len - kGC * chunk(c)) : 0;
             const int64_t at = start + (int64_t)kGC * max(chunk(c), 0);
-            const int gates = wave == C::W_STAGE && rows > 0 ? ((rows - 1) * a.hv + 1) * 4 : 0;
             load_rows<C::K::PPT, DK / 8>(y.k, a.k + at * a.ks + (int64_t)hk * DK, a.ks, rows, st);
             load_rows<C::K::PPT, DK / 8>(y.q, a.q + at * a.qs + (int64_t)hk * DK, a.qs, rows, st);
             load_rows<C::V::PPT, C::NV / 8>(y.o, a.d_out + at * os + (int64_t)h * a.dv + col0, os, rows, st);
-            y.la = bload4f(rsrc(a.la + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
-            y.be = bload4f(rsrc(a.be + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
         };
         auto stage = [&](const Staged& y, int c) {
             unsigned char* Ot = buf(C::O_O, C::V::SIZE, c);
@@ -143,19 +139,6 @@ __device__ __forceinline__ void gdn_walk_back(const WArgs& a, const GdnTable& ta
             for (int i = 0; i < C::V::PPT; ++i) {
                 const int e = st + 256 * i;
                 if (e < C::V::PIECES) lds_st(Ot + (e / (C::NV / 8)) * C::V::RS + (e % (C::NV / 8)) * 16, y.o[i]);
-            }
-            if (wave == C::W_STAGE) {
-                const double G = wave_scan_f64(log2_decay(y.la)), GC = __shfl(G, 63);
-                const float hi = (float)G, eg = __builtin_amdgcn_exp2f(hi);
-                unsigned char* gv = buf(C::O_G, GateVec::SIZE, c);
-                lds_st(gv + GateVec::HI + 4 * lane, hi);
-                lds_st(gv + GateVec::LO + 4 * lane, (float)(G - (double)hi));
-                lds_st(gv + GateVec::BE + 4 * lane, y.be);
-                unsigned char* vec = buf(C::O_VEC, C::V_SIZE, c);
-                lds_st(vec + C::V_ER + 4 * lane, __builtin_amdgcn_exp2f((float)(GC - G)));
-                lds_st(vec + C::V_BG + 4 * lane, -y.be * eg);
-                lds_st(vec + C::V_EG + 4 * lane, a.scale * eg);
-                if (lane == 0) lds_st(vec + C::V_GC, __builtin_amdgcn_exp2f((float)GC));
             }
         };
         unroll<0, R>([&](auto J) {
@@ -197,6 +180,38 @@ __device__ __forceinline__ void gdn_walk_back(const WArgs& a, const GdnTable& ta
             lds_barrier();
         }
         drain();
+        return;
+    }
+    if (wave == C::W_GATE) {
+        float la[R], be[R];
+        auto load = [&](float& x, float& y, int c) {
+            const int rows = c < nch ? min(kGC, len - kGC * chunk(c)) : 0;
+            const int64_t at = start + (int64_t)kGC * max(chunk(c), 0);
+            const int gates = rows > 0 ? ((rows - 1) * a.hv + 1) * 4 : 0;
+            x = bload4f(rsrc(a.la + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
+            y = bload4f(rsrc(a.be + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
+        };
+        unroll<0, R>([&](auto J) { load(la[decltype(J)::value], be[decltype(J)::value], decltype(J)::value); });
+        for (int c = 0; c < passes; c += R) {
+            unroll<0, R>([&](auto J) {
+                constexpr int j = decltype(J)::value;
+                const double G = wave_scan_f64(log2_decay(la[j])), GC = __shfl(G, 63);
+                const float hi = (float)G, eg = __builtin_amdgcn_exp2f(hi);
+                unsigned char* gv = buf(C::O_G, GateVec::SIZE, c + j);
+                lds_st(gv + GateVec::HI + 4 * lane, hi);
+                lds_st(gv + GateVec::LO + 4 * lane, (float)(G - (double)hi));
+                lds_st(gv + GateVec::BE + 4 * lane, be[j]);
+                unsigned char* vec = buf(C::O_VEC, C::V_SIZE, c + j);
+                lds_st(vec + C::V_ER + 4 * lane, __builtin_amdgcn_exp2f((float)(GC - G)));
+                lds_st(vec + C::V_BG + 4 * lane, -be[j] * eg);
+                lds_st(vec + C::V_EG + 4 * lane, a.scale * eg);
+                if (lane == 0) lds_st(vec + C::V_GC, __builtin_amdgcn_exp2f((float)GC));
+                load(la[j], be[j], c + j + R);
+                __builtin_amdgcn_sched_barrier(0);
+                lds_barrier();
+                lds_barrier();
+            });
+        }
         return;
     }
     if (wave >= C::W_GRAM) {

@@ -20,8 +20,8 @@ int gdn_recurrent_nv(int dv, int64_t pairs, int tokens, int cu_count) {
 int gdn_prefill_nv(int dv, int64_t pairs, int cu_count) {
     // One workgroup runs per compute unit at a time (its LDS): the columns are split in halves
     // until the (sequence, head) pairs cover every unit once, down to one 16-column block.  A
-    // narrower slice has a shorter step: 16384 tokens with 8 heads, 128 columns, 441 us at 16
-    // columns per workgroup, 487 at 32.  But every slice stages the keys: 23 sequences of up to
+    // narrower slice has a shorter step: 16384 tokens with 8 heads, 128 columns, 442 us at 16
+    // columns per workgroup, 472 at 32.  But every slice stages the keys: 23 sequences of up to
     // 4097 tokens, 32 heads of 128 columns: 309 us at 128 columns, 438 at 64, 655 at 32.
     int nv = dv;
     while (nv > 16 && pairs * (dv / nv) < cu_count) nv /= 2;

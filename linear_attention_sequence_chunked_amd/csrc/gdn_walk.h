@@ -17,7 +17,8 @@
 // The loop's passes have two phases, each ended by a workgroup barrier (LDS only: loads and
 // stores stay in flight).  Pass c:
 //              phase A                             phase B
-//   stage      K, Q, V, decays of chunk c          (loads of c+1 in flight)
+//   stage      K, Q, V of chunk c                  (loads of c+1 in flight)
+//   gates      its decays
 //   inverse    (I + A)'s halves: join of c-1       tiles and substitution of c
 //   gram       P of c-1 within the halves          A and P below the halves of c
 //   chain      K S of c-1                          X, U of c-1, the state behind it
@@ -25,7 +26,10 @@
 // K, Q, V, the decays and the matrices are double-buffered; S and U reach the out wave as the
 // fp16 operands they are, through LDS.  Two forms:
 //  * narrow (16 or 32 columns, few chains: the step's latency is the launch's time): every row
-//    above has waves of its own (4, 2, 2, one per 16 columns, 1);
+//    above has waves of its own (4, 1, 2, 2, one per 16 columns, 1).  The decays' wave is apart
+//    from the staging ones, the phase's longest: one sequence of 131072 tokens with 32 heads of
+//    128 x 128, 16 columns per workgroup, 3.54 ms (1.73 us a chunk) against 3.73; four of 4096
+//    with 16 heads, 32 columns, 153 to 157 us (2.4 us a chunk) either way;
 //  * wide (64 or 128 columns): the chain waves (two column blocks each at 128) do the out
 //    wave's work on their own registers, and four producer waves stage in phase A and invert
 //    or form Gram tiles, two and two, in phase B; more waves would not have the registers.
@@ -58,9 +62,10 @@ struct GCfg {
     // 32 columns; one otherwise (the shortest step)
     static constexpr int CPW = NCB >= 8 ? 2 : 1;
     static constexpr int NCHAIN = NCB / CPW;
-    // wave numbers: chain, stage (the wide form's producers), inverse, gram, out
+    // wave numbers: chain, stage (the wide form's producers), inverse, gram, out, gates
     static constexpr int W_STAGE = NCHAIN, W_INV = NARROW ? W_STAGE + 4 : W_STAGE, W_GRAM = W_INV + 2,
-                         W_OUT = W_GRAM + 2, WAVES = W_OUT + (NARROW ? 1 : 0), THREADS = 64 * WAVES;
+                         W_OUT = W_GRAM + 2, W_GATE = NARROW ? W_OUT + 1 : W_STAGE, WAVES = W_OUT + (NARROW ? 2 : 0),
+                         THREADS = 64 * WAVES;
     typedef KeyTile<DK> K;
     typedef ValueTile<NV> V;
     // matrices, as operand fragments (16 bytes per lane): row tiles 0 and 1 of T's upper half,
@@ -156,15 +161,34 @@ __device__ __forceinline__ void gdn_walk(const PArgs& a, const GdnTable& tab, in
     // No branch may lie between a load and its use: the compiler would wait for every load in
     // flight there.  So chunks behind the last, and the gates in all waves but one, are loaded over
     // an empty range (nothing is read, the registers get zeros).
+    auto load_gates = [&](float& la, float& be, int c) {
+        const int rows = min(kGC, len - kGC * c);
+        const int64_t at = start + (int64_t)kGC * c;
+        const int gates = wave == C::W_GATE && rows > 0 ? ((rows - 1) * a.hv + 1) * 4 : 0;
+        la = bload4f(rsrc(a.la + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
+        be = bload4f(rsrc(a.be + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
+    };
+    auto put_gates = [&](float la, float be, int c) {
+        const double G = wave_scan_f64(log2_decay(la)), GC = __shfl(G, 63);
+        const float hi = (float)G, eg = __builtin_amdgcn_exp2f(hi);
+        unsigned char* gv = buf(C::O_G, GateVec::SIZE, c);
+        lds_st(gv + GateVec::HI + 4 * lane, hi);
+        lds_st(gv + GateVec::LO + 4 * lane, (float)(G - (double)hi));
+        lds_st(gv + GateVec::BE + 4 * lane, be);
+        unsigned char* vec = buf(C::O_VEC, C::V_SIZE, c);
+        lds_st(vec + C::V_EG + 4 * lane, eg);
+        lds_st(vec + C::V_BE + 4 * lane, be * eg);
+        lds_st(vec + C::V_B + 4 * lane, kPre * be);
+        lds_st(vec + C::V_ER + 4 * lane, __builtin_amdgcn_exp2f((float)(GC - G)));
+        if (lane == 0) lds_st(vec + C::V_GC, __builtin_amdgcn_exp2f((float)GC));
+    };
     auto load = [&](Staged& x, int c) {
         const int rows = min(kGC, len - kGC * c);
         const int64_t at = start + (int64_t)kGC * c;
-        const int gates = wave == C::W_STAGE && rows > 0 ? ((rows - 1) * a.hv + 1) * 4 : 0;
         load_rows<C::K::PPT, DK / 8>(x.k, a.k + at * a.ks + (int64_t)hk * DK, a.ks, rows, st);
         if constexpr (C::OUT) load_rows<C::K::PPT, DK / 8>(x.q, a.q + at * a.qs + (int64_t)hk * DK, a.qs, rows, st);
         load_rows<C::V::PPT, C::NV / 8>(x.v, a.v + at * a.vs + (int64_t)h * a.dv + col0, a.vs, rows, st);
-        x.la = bload4f(rsrc(a.la + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
-        x.be = bload4f(rsrc(a.be + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
+        if constexpr (!C::NARROW) load_gates(x.la, x.be, c);
     };
     auto stage = [&](const Staged& x, int c) {
         unsigned char* Vt = buf(C::O_V, C::V::SIZE, c);
@@ -175,19 +199,8 @@ __device__ __forceinline__ void gdn_walk(const PArgs& a, const GdnTable& tab, in
             const int e = st + 256 * i;
             if (e < C::V::PIECES) lds_st(Vt + (e / (C::NV / 8)) * C::V::RS + (e % (C::NV / 8)) * 16, x.v[i]);
         }
-        if (wave == C::W_STAGE) {
-            const double G = wave_scan_f64(log2_decay(x.la)), GC = __shfl(G, 63);
-            const float hi = (float)G, eg = __builtin_amdgcn_exp2f(hi);
-            unsigned char* gv = buf(C::O_G, GateVec::SIZE, c);
-            lds_st(gv + GateVec::HI + 4 * lane, hi);
-            lds_st(gv + GateVec::LO + 4 * lane, (float)(G - (double)hi));
-            lds_st(gv + GateVec::BE + 4 * lane, x.be);
-            unsigned char* vec = buf(C::O_VEC, C::V_SIZE, c);
-            lds_st(vec + C::V_EG + 4 * lane, eg);
-            lds_st(vec + C::V_BE + 4 * lane, x.be * eg);
-            lds_st(vec + C::V_B + 4 * lane, kPre * x.be);
-            lds_st(vec + C::V_ER + 4 * lane, __builtin_amdgcn_exp2f((float)(GC - G)));
-            if (lane == 0) lds_st(vec + C::V_GC, __builtin_amdgcn_exp2f((float)GC));
+        if constexpr (!C::NARROW) {
+            if (wave == C::W_GATE) put_gates(x.la, x.be, c);
         }
     };
     unsigned char* isc = smem + C::O_INV + (wave - C::W_INV) * InvScratch::SIZE;  // inverse waves
@@ -306,6 +319,21 @@ __device__ __forceinline__ void gdn_walk(const PArgs& a, const GdnTable& tab, in
                 constexpr int j = decltype(J)::value;
                 stage(x[j], c + j);
                 load(x[j], c + j + R);
+                __builtin_amdgcn_sched_barrier(0);
+                lds_barrier();
+                lds_barrier();
+            });
+        }
+        return;
+    }
+    if (C::NARROW && wave == C::W_GATE) {
+        float la[R], be[R];
+        unroll<0, R>([&](auto J) { load_gates(la[decltype(J)::value], be[decltype(J)::value], decltype(J)::value); });
+        for (int c = 0; c < passes; c += R) {
+            unroll<0, R>([&](auto J) {
+                constexpr int j = decltype(J)::value;
+                put_gates(la[j], be[j], c + j);
+                load_gates(la[j], be[j], c + j + R);
                 __builtin_amdgcn_sched_barrier(0);
                 lds_barrier();
                 lds_barrier();
@@ -495,7 +523,7 @@ __device__ __forceinline__ void gdn_walk(const PArgs& a, const GdnTable& tab, in
 #pragma unroll
             for (int t = 0; t < 4; ++t) Y[cb][t] = O[cb][t] = zero4();
         // The conversions of step p + 1 are issued between the products of step p: the vector unit works under the matrix
-        // unit's time (one sequence of 131072 tokens, 32 heads: 3.76 ms; in front of the products 3.87).
+        // unit's time (one sequence of 131072 tokens, 32 heads: 3% less than in front of the products).
         f16x8 sh[2][CPW], sl[2][CPW];
         auto split_state = [&](auto PI) {
             constexpr int p = decltype(PI)::value;
