@@ -122,14 +122,19 @@ __device__ __forceinline__ void gdn_walk_back(const WArgs& a, const GdnTable& ta
         };
         Staged x[R];
         const int st = tid - 64 * C::W_STAGE;
+        const int64_t at = start + (int64_t)kGC * max(nch - 1, 0);
+        const bf16 *kp = a.k + at * a.ks + (int64_t)hk * DK, *qp = a.q + at * a.qs + (int64_t)hk * DK,
+                   *op = a.d_out + at * os + (int64_t)h * a.dv + col0;
+        // Each call loads the chunk before.  (Those before the first over an empty range: no branch
+        // between a load and its use.)
         auto load = [&](Staged& y, int c) {
-            // (chunks before the first are loaded over an empty range: no branch between a load and
-            // its use)
             const int rows = c < nch ? min(kGC, len - kGC * chunk(c)) : 0;
-            const int64_t at = start + (int64_t)kGC * max(chunk(c), 0);
-            load_rows<C::K::PPT, DK / 8>(y.k, a.k + at * a.ks + (int64_t)hk * DK, a.ks, rows, st);
-            load_rows<C::K::PPT, DK / 8>(y.q, a.q + at * a.qs + (int64_t)hk * DK, a.qs, rows, st);
-            load_rows<C::V::PPT, C::NV / 8>(y.o, a.d_out + at * os + (int64_t)h * a.dv + col0, os, rows, st);
+            load_rows<C::K::PPT, DK / 8>(y.k, kp, a.ks, rows, st);
+            load_rows<C::K::PPT, DK / 8>(y.q, qp, a.qs, rows, st);
+            load_rows<C::V::PPT, C::NV / 8>(y.o, op, os, rows, st);
+            kp -= kGC * a.ks;
+            qp -= kGC * a.qs;
+            op -= (int64_t)kGC * os;
         };
         auto stage = [&](const Staged& y, int c) {
             unsigned char* Ot = buf(C::O_O, C::V::SIZE, c);

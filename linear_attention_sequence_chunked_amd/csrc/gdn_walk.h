@@ -161,12 +161,19 @@ __device__ __forceinline__ void gdn_walk(const PArgs& a, const GdnTable& tab, in
     // No branch may lie between a load and its use: the compiler would wait for every load in
     // flight there.  So chunks behind the last, and the gates in all waves but one, are loaded over
     // an empty range (nothing is read, the registers get zeros).
-    auto load_gates = [&](float& la, float& be, int c) {
-        const int rows = min(kGC, len - kGC * c);
-        const int64_t at = start + (int64_t)kGC * c;
+    // Each call loads the next chunk (addresses are added up, not multiplied out).
+    int rows_left = len, gates_left = len;
+    const bf16 *kp = a.k + start * a.ks + (int64_t)hk * DK, *qp = a.q + start * a.qs + (int64_t)hk * DK,
+               *vp = a.v + start * a.vs + (int64_t)h * a.dv + col0;
+    const float *lap = a.la + start * a.hv + h, *bep = a.be + start * a.hv + h;
+    auto load_gates = [&](float& la, float& be) {
+        const int rows = min(kGC, gates_left);
         const int gates = wave == C::W_GATE && rows > 0 ? ((rows - 1) * a.hv + 1) * 4 : 0;
-        la = bload4f(rsrc(a.la + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
-        be = bload4f(rsrc(a.be + at * a.hv + h, gates), (uint32_t)(lane * a.hv * 4));
+        la = bload4f(rsrc(lap, gates), (uint32_t)(lane * a.hv * 4));
+        be = bload4f(rsrc(bep, gates), (uint32_t)(lane * a.hv * 4));
+        gates_left -= kGC;
+        lap += (int64_t)kGC * a.hv;
+        bep += (int64_t)kGC * a.hv;
     };
     auto put_gates = [&](float la, float be, int c) {
         const double G = wave_scan_f64(log2_decay(la)), GC = __shfl(G, 63);
@@ -182,13 +189,16 @@ __device__ __forceinline__ void gdn_walk(const PArgs& a, const GdnTable& tab, in
         lds_st(vec + C::V_ER + 4 * lane, __builtin_amdgcn_exp2f((float)(GC - G)));
         if (lane == 0) lds_st(vec + C::V_GC, __builtin_amdgcn_exp2f((float)GC));
     };
-    auto load = [&](Staged& x, int c) {
-        const int rows = min(kGC, len - kGC * c);
-        const int64_t at = start + (int64_t)kGC * c;
-        load_rows<C::K::PPT, DK / 8>(x.k, a.k + at * a.ks + (int64_t)hk * DK, a.ks, rows, st);
-        if constexpr (C::OUT) load_rows<C::K::PPT, DK / 8>(x.q, a.q + at * a.qs + (int64_t)hk * DK, a.qs, rows, st);
-        load_rows<C::V::PPT, C::NV / 8>(x.v, a.v + at * a.vs + (int64_t)h * a.dv + col0, a.vs, rows, st);
-        if constexpr (!C::NARROW) load_gates(x.la, x.be, c);
+    auto load = [&](Staged& x) {
+        const int rows = min(kGC, rows_left);
+        load_rows<C::K::PPT, DK / 8>(x.k, kp, a.ks, rows, st);
+        if constexpr (C::OUT) load_rows<C::K::PPT, DK / 8>(x.q, qp, a.qs, rows, st);
+        load_rows<C::V::PPT, C::NV / 8>(x.v, vp, a.vs, rows, st);
+        if constexpr (!C::NARROW) load_gates(x.la, x.be);
+        rows_left -= kGC;
+        kp += kGC * a.ks;
+        qp += kGC * a.qs;
+        vp += kGC * a.vs;
     };
     auto stage = [&](const Staged& x, int c) {
         unsigned char* Vt = buf(C::O_V, C::V::SIZE, c);
@@ -280,11 +290,11 @@ __device__ __forceinline__ void gdn_walk(const PArgs& a, const GdnTable& tab, in
     if (!C::NARROW && wave >= C::W_STAGE) {
         // ---------------------------------------------------------------- wide: producers
         Staged x;
-        load(x, 0);
+        load(x);
         for (int c = 0; c <= nch; ++c) {
             if (c < nch) {
                 stage(x, c);
-                load(x, c + 1);
+                load(x);
             }
             lds_barrier();
             if (c < nch) {
@@ -311,14 +321,14 @@ __device__ __forceinline__ void gdn_walk(const PArgs& a, const GdnTable& tab, in
         // them.)
         Staged x[R];
         unroll<0, R>([&](auto J) {
-            load(x[decltype(J)::value], decltype(J)::value);
+            load(x[decltype(J)::value]);
             __builtin_amdgcn_sched_barrier(0);  // in this order
         });
         for (int c = 0; c < passes; c += R) {
             unroll<0, R>([&](auto J) {
                 constexpr int j = decltype(J)::value;
                 stage(x[j], c + j);
-                load(x[j], c + j + R);
+                load(x[j]);
                 __builtin_amdgcn_sched_barrier(0);
                 lds_barrier();
                 lds_barrier();
@@ -328,12 +338,12 @@ __device__ __forceinline__ void gdn_walk(const PArgs& a, const GdnTable& tab, in
     }
     if (C::NARROW && wave == C::W_GATE) {
         float la[R], be[R];
-        unroll<0, R>([&](auto J) { load_gates(la[decltype(J)::value], be[decltype(J)::value], decltype(J)::value); });
+        unroll<0, R>([&](auto J) { load_gates(la[decltype(J)::value], be[decltype(J)::value]); });
         for (int c = 0; c < passes; c += R) {
             unroll<0, R>([&](auto J) {
                 constexpr int j = decltype(J)::value;
                 put_gates(la[j], be[j], c + j);
-                load_gates(la[j], be[j], c + j + R);
+                load_gates(la[j], be[j]);
                 __builtin_amdgcn_sched_barrier(0);
                 lds_barrier();
                 lds_barrier();
